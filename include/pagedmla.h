@@ -72,6 +72,15 @@ extern "C" {
 #define MLA_FLAG_ONE_SM 8u        /* mla_decode_paged: above 16 rows, the 1-SM 64-row tcgen05
                                      kernel even where the CTA-pair kernel applies */
 
+/* Element types of the operators that take more than one. */
+#define MLA_DTYPE_BF16 0
+#define MLA_DTYPE_F16 1
+#define MLA_DTYPE_F32 2
+
+#define MLA_ROPE_HALF 1u          /* rotary pairs are columns (i, i + n), not (2i, 2i + 1) */
+#define MLA_ROPE_INVERSE 2u       /* mla_rope: turn by the negative angle (the gradient) */
+#define MLA_ROPE_POS64 4u         /* positions are int64, not int32 */
+
 typedef struct CUstream_st *mla_stream_t; /* identical to cudaStream_t */
 
 /*
@@ -322,6 +331,132 @@ MLA_API int mla_absorb_query(const void *q_nope, const int64_t nope_strides[2], 
                              mla_stream_t stream);
 MLA_API int mla_absorb_output(const void *o_latent, const int64_t latent_strides[2], const void *w_uv, int tokens,
                               int heads, void *out, mla_stream_t stream);
+
+/*
+ * mla_rope -- rotary positions.  Of every (token, head) row of `width` columns the last
+ * 2 * pairs are rotated, in pairs, by the angle a_i = position * inv_freq[i]:
+ *   y0 = magnitude * (x0 cos a_i - x1 sin a_i),  y1 = magnitude * (x0 sin a_i + x1 cos a_i)
+ * Pair i is columns (2i, 2i + 1) of them, with MLA_ROPE_HALF columns (i, i + pairs).  The
+ * columns in front pass through.  MLA_ROPE_INVERSE turns by -a_i: with the same magnitude that
+ * is the gradient of the call without it.  For the latent decode: the 64 rope columns of
+ * q_rope before mla_absorb_query (the cached rope columns are turned by mla_cache_write).
+ *   x          device, `dtype` (MLA_DTYPE_*), element (t, h, c) at t * x_strides[0] +
+ *              h * x_strides[1] + c; strides >= 0
+ *   positions  device int32 [tokens] (int64 with MLA_ROPE_POS64), any value
+ *   inv_freq   device fp64 [pairs]; a scaling for long contexts is part of these and of
+ *              `magnitude`.  Angles are reduced in fp64, so far positions keep their accuracy
+ *   out        device, `dtype`, element (t, h, c) as x with out_strides.  Either x itself (same
+ *              address and strides: in place, only the rotated columns are touched) or memory
+ *              that does not overlap x.  Rows of out must not overlap each other
+ * Rotated in fp32, rounded once.  Rows whose sizes, strides and addresses are multiples of 16
+ * bytes are moved 16 bytes at a time, others an element at a time.  tokens = 0 enqueues
+ * nothing.  tokens <= 2^31, heads <= 65535, pairs in [1, 512], width <= 65536.
+ * A programmatic dependent launch that waits for the kernel before it.
+ * Errors: MLA_ERR_ARG, MLA_ERR_CUDA.
+ */
+MLA_API int mla_rope(const void *x, const int64_t x_strides[2], int dtype, int64_t tokens, int heads, int width,
+                     int pairs, const void *positions, const double *inv_freq, float magnitude, unsigned flags,
+                     void *out, const int64_t out_strides[2], mla_stream_t stream);
+
+/*
+ * mla_cache_slots -- where a step's new tokens go: the plan of mla_cache_write, computed once
+ * per step for all layers.  The new tokens of all sequences are numbered one after another,
+ * those of sequence b are row_ptr[b] .. row_ptr[b + 1) and are the last of its
+ * cache_seqlens[b] entries (as the s_q new tokens of the decode are).  For token t at position
+ * x of sequence b: positions[t] = x and slots[t] = block_table[b][x / 64] * 64 + x % 64.
+ * Tokens outside [row_ptr[0], row_ptr[batch]) (the padding of a fixed-size step), positions
+ * below 0 or past the table's width, and pages outside [0, num_pages) get slot -1, position 0.
+ * Rows of a prefix to read back are listed by the same call (all L_b tokens as "new").
+ *   row_ptr       device int32 [batch + 1], non-decreasing
+ *   block_table   device int32 [batch][table_width] with row stride block_table_stride
+ *   slots         device int64 [tokens], written; positions device int32 [tokens], written
+ * tokens = 0 enqueues nothing.  Errors: MLA_ERR_ARG, MLA_ERR_CUDA.
+ */
+MLA_API int mla_cache_slots(const int32_t *row_ptr, const int32_t *cache_seqlens, int batch,
+                            const int32_t *block_table, int64_t block_table_stride, int table_width,
+                            int64_t num_pages, int64_t tokens, int64_t *slots, int32_t *positions,
+                            mla_stream_t stream);
+
+/*
+ * mla_cache_write / mla_cache_write_fp8 -- new tokens' latent rows into the paged cache, in the
+ * decode's formats.  Per token t and latent head h:
+ *   columns 0..511    latent[t][h], or with norm_weight latent * weight / sqrt(mean(latent^2) + eps)
+ *   columns 512..575  rope[t][h], or with inv_freq its 32 pairs turned as by mla_rope
+ * rounded to bf16 in k_cache, or stored as E4M3 codes and one scale: scale = max|row| / 448 (1
+ * for a row of zeros), code = row / scale to nearest.  The row is formed in fp32; an infinity
+ * or NaN becomes a NaN code and does not enter the scale.
+ *   latent, rope  device, `dtype` (MLA_DTYPE_*), element (t, h, c) at t * strides[0] + h *
+ *                 strides[1] + c (for instance the two column ranges of one projection);
+ *                 strides non-negative multiples of 8, 16-byte aligned
+ *   norm_weight   device [512] of `dtype`, 16-byte aligned, or NULL: no norm
+ *   positions, inv_freq [32], magnitude, flags (MLA_ROPE_HALF, MLA_ROPE_POS64): as in mla_rope;
+ *                 inv_freq NULL: the rope columns are stored as they are (positions unused)
+ *   slots         device int64 [tokens]: page * 64 + offset.  Tokens with a slot outside
+ *                 [0, num_pages * 64) are skipped.  Slots must be distinct: where one is listed
+ *                 twice, the row ends as an unspecified mixture of the two
+ *   k_cache / k8, k_scale  the pool, as in mla_decode_paged / mla_decode_paged_fp8; only the
+ *                 listed rows are written
+ * tokens = 0 enqueues nothing.  tokens * h_kv <= 2^31.  Programmatic dependent launches that
+ * wait for the kernel before them.  Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED (page_size),
+ * MLA_ERR_CUDA.
+ */
+MLA_API int mla_cache_write(const void *latent, const int64_t latent_strides[2], const void *rope,
+                            const int64_t rope_strides[2], int dtype, int64_t tokens, int h_kv,
+                            const void *norm_weight, float eps, const void *positions, const double *inv_freq,
+                            float magnitude, unsigned flags, const int64_t *slots, void *k_cache, int64_t num_pages,
+                            int page_size, mla_stream_t stream);
+MLA_API int mla_cache_write_fp8(const void *latent, const int64_t latent_strides[2], const void *rope,
+                                const int64_t rope_strides[2], int dtype, int64_t tokens, int h_kv,
+                                const void *norm_weight, float eps, const void *positions, const double *inv_freq,
+                                float magnitude, unsigned flags, const int64_t *slots, void *k8, float *k_scale,
+                                int64_t num_pages, int page_size, mla_stream_t stream);
+
+/*
+ * mla_cache_read / mla_cache_read_fp8 -- rows of the paged cache by slot, in list order, as bf16
+ * (the FP8 cache: scale * code, rounded once): a cached prefix for the prompt's attention, or
+ * rows to move elsewhere.
+ *   slots  device int64 [tokens]; a slot outside [0, num_pages * 64) gives a row of zeros; a
+ *          slot may be listed more than once
+ *   out    device bf16, element (t, h, c) at t * out_strides[0] + h * out_strides[1] + c, 576
+ *          columns, written; strides non-negative multiples of 8, 16-byte aligned; rows must not
+ *          overlap each other or the cache
+ * tokens = 0 enqueues nothing.  tokens * h_kv <= 2^31.  Programmatic dependent launches that
+ * wait for the kernel before them.  Errors: MLA_ERR_ARG, MLA_ERR_UNSUPPORTED (page_size),
+ * MLA_ERR_CUDA.
+ */
+MLA_API int mla_cache_read(const void *k_cache, int64_t num_pages, int page_size, int h_kv, const int64_t *slots,
+                           int64_t tokens, void *out, const int64_t out_strides[2], mla_stream_t stream);
+MLA_API int mla_cache_read_fp8(const void *k8, const float *k_scale, int64_t num_pages, int page_size, int h_kv,
+                               const int64_t *slots, int64_t tokens, void *out, const int64_t out_strides[2],
+                               mla_stream_t stream);
+
+/*
+ * mla_verify_draft -- which drafted tokens the target keeps, and the token after them, from
+ * given uniform numbers (speculative sampling: the tokens follow the target's distribution).
+ * Per sequence b with n = num_drafts[b] drafts d_i, target rows p_0..p_n and draft rows q_i:
+ *   d_i is accepted while uniform[b][i] * q_i(d_i) < p_i(d_i); accepted[b] = r of them
+ *   the next token is drawn from max(p_r - q_r, 0) if r < n, else from p_n: the lowest j whose
+ *   running sum exceeds uniform_new[b] times the whole sum (fp64 products and sums)
+ * draft_probs NULL: the drafts were chosen with certainty (q_i is 1 at d_i, 0 elsewhere).
+ * Entries that are not finite positive numbers have no weight; where max(p_r - q_r, 0) has none
+ * anywhere the token is drawn from p_r, and if p_r has none either it is -1.  A draft outside
+ * [0, vocab) is rejected.
+ *   target_probs  device, `dtype` (MLA_DTYPE_*), element (b, i, j) at b * target_strides[0] +
+ *                 i * target_strides[1] + j, i in [0, drafts]; need not sum to one
+ *   draft_probs   the same with i in [0, drafts), or NULL
+ *   draft_tokens  device int32 [batch][drafts], contiguous; uniform device fp32 of that shape
+ *   uniform_new   device fp32 [batch], in [0, 1)
+ *   num_drafts    device int32 [batch], clamped to [0, drafts], or NULL: `drafts` everywhere
+ *   accepted      device int32 [batch], written
+ *   tokens        device int32 [batch][drafts + 1], written: the accepted drafts, the next
+ *                 token, then -1
+ * drafts >= 1, vocab >= 1, strides >= 0, batch <= 2^24.  A programmatic dependent launch that
+ * waits for the kernel before it.  Errors: MLA_ERR_ARG, MLA_ERR_CUDA.
+ */
+MLA_API int mla_verify_draft(const void *target_probs, const int64_t target_strides[2], const void *draft_probs,
+                             const int64_t draft_strides[2], int dtype, const int32_t *draft_tokens,
+                             const float *uniform, const float *uniform_new, const int32_t *num_drafts, int batch,
+                             int drafts, int vocab, int32_t *accepted, int32_t *tokens, mla_stream_t stream);
 
 /*
  * mla_query_status -- synchronise `stream`, read and clear the workspace status block.

@@ -163,6 +163,93 @@ int check_common(int batch, int s_q, int h_q, int h_kv, int dv) {
   return MLA_OK;
 }
 
+int check_dtype(int dtype) {
+  if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_F16 && dtype != MLA_DTYPE_F32)
+    return fail(MLA_ERR_ARG, "unknown element type %d", dtype);
+  return MLA_OK;
+}
+
+int check_rows(int64_t tokens, int h_kv, int64_t num_pages, int page_size) {
+  if (tokens < 0 || h_kv < 1) return fail(MLA_ERR_ARG, "tokens must be >= 0 and h_kv >= 1");
+  if (tokens > (int64_t(1) << 31) / h_kv) return fail(MLA_ERR_ARG, "tokens * h_kv must be <= 2^31");
+  if (page_size != kPage) return fail(MLA_ERR_UNSUPPORTED, "page_size must be %d (got %d)", kPage, page_size);
+  if (num_pages < 1 || num_pages > (int64_t(1) << 25)) return fail(MLA_ERR_ARG, "num_pages must be in [1, 2^25]");
+  return MLA_OK;
+}
+
+int cache_write(const void *latent, const int64_t *latent_strides, const void *rope, const int64_t *rope_strides,
+                int dtype, int64_t tokens, int h_kv, const void *norm_weight, float eps, const void *positions,
+                const double *inv_freq, float magnitude, unsigned flags, const int64_t *slots, void *cache,
+                float *k_scale, bool fp8, int64_t num_pages, int page_size, mla_stream_t stream) {
+  int rc = check_rows(tokens, h_kv, num_pages, page_size);
+  if (rc) return rc;
+  rc = check_dtype(dtype);
+  if (rc) return rc;
+  if (flags & ~(MLA_ROPE_HALF | MLA_ROPE_POS64)) return fail(MLA_ERR_ARG, "unknown flags 0x%x", flags);
+  if (norm_weight && !(eps >= 0.f && std::isfinite(eps))) return fail(MLA_ERR_ARG, "eps must be >= 0 and finite");
+  if (inv_freq && !std::isfinite(magnitude)) return fail(MLA_ERR_ARG, "magnitude must be finite");
+  if (tokens == 0) return MLA_OK;
+  if (!latent || !latent_strides || !rope || !rope_strides || !slots || !cache || (fp8 && !k_scale) ||
+      (inv_freq && !positions))
+    return fail(MLA_ERR_ARG, "null pointer argument");
+  for (int i = 0; i < 2; ++i)
+    if (latent_strides[i] < 0 || latent_strides[i] % 8 || rope_strides[i] < 0 || rope_strides[i] % 8)
+      return fail(MLA_ERR_ARG, "strides must be non-negative multiples of 8 elements");
+  if (!aligned(latent, 16) || !aligned(rope, 16) || !aligned(norm_weight, 16) || !aligned(cache, 16) ||
+      !aligned(k_scale, 16) || !aligned(slots, 8) || !aligned(inv_freq, 8) ||
+      !aligned(positions, flags & MLA_ROPE_POS64 ? 8 : 4))
+    return fail(MLA_ERR_ARG, "latent, rope, norm_weight and the cache must be 16-byte aligned, slots and inv_freq 8-byte");
+  CacheWriteParams p;
+  p.latent = latent;
+  p.rope = rope;
+  p.l_t = latent_strides[0];
+  p.l_h = latent_strides[1];
+  p.r_t = rope_strides[0];
+  p.r_h = rope_strides[1];
+  p.tokens = tokens;
+  p.h_kv = h_kv;
+  p.weight = norm_weight;
+  p.eps = eps;
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.magnitude = magnitude;
+  p.pos64 = (flags & MLA_ROPE_POS64) != 0;
+  p.half = (flags & MLA_ROPE_HALF) != 0;
+  p.slots = slots;
+  p.cache = cache;
+  p.scale = k_scale;
+  p.num_slots = num_pages * kPage;
+  cudaError_t e = launch_cache_write(p, dtype, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache write kernel launch");
+  return MLA_OK;
+}
+
+int cache_read(const void *cache, const float *k_scale, bool fp8, int64_t num_pages, int page_size, int h_kv,
+               const int64_t *slots, int64_t tokens, void *out, const int64_t *out_strides, mla_stream_t stream) {
+  int rc = check_rows(tokens, h_kv, num_pages, page_size);
+  if (rc) return rc;
+  if (tokens == 0) return MLA_OK;
+  if (!cache || (fp8 && !k_scale) || !slots || !out || !out_strides) return fail(MLA_ERR_ARG, "null pointer argument");
+  for (int i = 0; i < 2; ++i)
+    if (out_strides[i] < 0 || out_strides[i] % 8)
+      return fail(MLA_ERR_ARG, "strides must be non-negative multiples of 8 elements");
+  if (!aligned(cache, 16) || !aligned(k_scale, 16) || !aligned(out, 16) || !aligned(slots, 8))
+    return fail(MLA_ERR_ARG, "the cache and out must be 16-byte aligned, slots 8-byte aligned");
+  CacheReadParams p;
+  p.cache = cache;
+  p.scale = k_scale;
+  p.num_slots = num_pages * kPage;
+  p.tokens = tokens;
+  p.h_kv = h_kv;
+  p.slots = slots;
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.o_t = out_strides[0];
+  p.o_h = out_strides[1];
+  cudaError_t e = launch_cache_read(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache read kernel launch");
+  return MLA_OK;
+}
+
 }  // namespace
 
 namespace pagedmla {
@@ -616,6 +703,137 @@ int mla_absorb_output(const void *o_latent, const int64_t latent_strides[2], con
                                     static_cast<const __nv_bfloat16 *>(w_uv), static_cast<__nv_bfloat16 *>(out), tokens,
                                     heads, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "output absorption launch");
+  return MLA_OK;
+}
+
+int mla_rope(const void *x, const int64_t x_strides[2], int dtype, int64_t tokens, int heads, int width, int pairs,
+             const void *positions, const double *inv_freq, float magnitude, unsigned flags, void *out,
+             const int64_t out_strides[2], mla_stream_t stream) {
+  if (tokens < 0 || heads < 1) return fail(MLA_ERR_ARG, "tokens must be >= 0 and heads >= 1");
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  if (pairs < 1 || pairs > 512 || width < 2 * pairs || width > 65536)
+    return fail(MLA_ERR_ARG, "pairs must be in [1, 512] and width in [2 * pairs, 65536] (got %d, %d)", pairs, width);
+  if (flags & ~(MLA_ROPE_HALF | MLA_ROPE_INVERSE | MLA_ROPE_POS64)) return fail(MLA_ERR_ARG, "unknown flags 0x%x", flags);
+  if (!std::isfinite(magnitude)) return fail(MLA_ERR_ARG, "magnitude must be finite");
+  if (tokens == 0) return MLA_OK;
+  if (!x || !x_strides || !positions || !inv_freq || !out || !out_strides)
+    return fail(MLA_ERR_ARG, "null pointer argument");
+  if (tokens > (int64_t(1) << 31) || heads > 65535) return fail(MLA_ERR_ARG, "too many tokens or heads");
+  for (int i = 0; i < 2; ++i)
+    if (x_strides[i] < 0 || out_strides[i] < 0) return fail(MLA_ERR_ARG, "strides must be non-negative");
+  const size_t size = dtype == MLA_DTYPE_F32 ? 4 : 2;
+  if (!aligned(x, size) || !aligned(out, size) || !aligned(inv_freq, 8) ||
+      !aligned(positions, flags & MLA_ROPE_POS64 ? 8 : 4))
+    return fail(MLA_ERR_ARG, "x, out, positions and inv_freq must be aligned to their element size");
+  const bool same = x == out;
+  if (same && (x_strides[0] != out_strides[0] || x_strides[1] != out_strides[1]))
+    return fail(MLA_ERR_ARG, "in place, out must have the strides of x");
+  RopeParams p;
+  p.x = x;
+  p.out = out;
+  p.x_t = x_strides[0];
+  p.x_h = x_strides[1];
+  p.o_t = out_strides[0];
+  p.o_h = out_strides[1];
+  p.tokens = tokens;
+  p.heads = heads;
+  p.width = width;
+  p.pairs = pairs;
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.magnitude = magnitude;
+  p.pos64 = (flags & MLA_ROPE_POS64) != 0;
+  p.inverse = (flags & MLA_ROPE_INVERSE) != 0;
+  p.copy_front = !same && width > 2 * pairs;
+  cudaError_t e = launch_rope(p, dtype, (flags & MLA_ROPE_HALF) != 0, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rotary kernel launch");
+  return MLA_OK;
+}
+
+int mla_cache_slots(const int32_t *row_ptr, const int32_t *cache_seqlens, int batch, const int32_t *block_table,
+                    int64_t block_table_stride, int table_width, int64_t num_pages, int64_t tokens, int64_t *slots,
+                    int32_t *positions, mla_stream_t stream) {
+  if (batch < 1 || tokens < 0) return fail(MLA_ERR_ARG, "batch must be >= 1 and tokens >= 0");
+  if (block_table_stride < 0 || table_width < 1)
+    return fail(MLA_ERR_ARG, "table_width must be >= 1 and block_table_stride non-negative");
+  if (num_pages < 1 || num_pages > (int64_t(1) << 25)) return fail(MLA_ERR_ARG, "num_pages must be in [1, 2^25]");
+  if (tokens > (int64_t(1) << 31)) return fail(MLA_ERR_ARG, "too many tokens");
+  if (tokens == 0) return MLA_OK;
+  if (!row_ptr || !cache_seqlens || !block_table || !slots || !positions)
+    return fail(MLA_ERR_ARG, "null pointer argument");
+  if (!aligned(slots, 8) || !aligned(positions, 4)) return fail(MLA_ERR_ARG, "slots must be 8-byte aligned");
+  cudaError_t e = launch_cache_slots(row_ptr, cache_seqlens, batch, block_table, block_table_stride, table_width,
+                                     num_pages, tokens, slots, positions, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache slot kernel launch");
+  return MLA_OK;
+}
+
+int mla_cache_write(const void *latent, const int64_t latent_strides[2], const void *rope,
+                    const int64_t rope_strides[2], int dtype, int64_t tokens, int h_kv, const void *norm_weight,
+                    float eps, const void *positions, const double *inv_freq, float magnitude, unsigned flags,
+                    const int64_t *slots, void *k_cache, int64_t num_pages, int page_size, mla_stream_t stream) {
+  return cache_write(latent, latent_strides, rope, rope_strides, dtype, tokens, h_kv, norm_weight, eps, positions,
+                     inv_freq, magnitude, flags, slots, k_cache, nullptr, false, num_pages, page_size, stream);
+}
+
+int mla_cache_write_fp8(const void *latent, const int64_t latent_strides[2], const void *rope,
+                        const int64_t rope_strides[2], int dtype, int64_t tokens, int h_kv, const void *norm_weight,
+                        float eps, const void *positions, const double *inv_freq, float magnitude, unsigned flags,
+                        const int64_t *slots, void *k8, float *k_scale, int64_t num_pages, int page_size,
+                        mla_stream_t stream) {
+  return cache_write(latent, latent_strides, rope, rope_strides, dtype, tokens, h_kv, norm_weight, eps, positions,
+                     inv_freq, magnitude, flags, slots, k8, k_scale, true, num_pages, page_size, stream);
+}
+
+int mla_cache_read(const void *k_cache, int64_t num_pages, int page_size, int h_kv, const int64_t *slots,
+                   int64_t tokens, void *out, const int64_t out_strides[2], mla_stream_t stream) {
+  return cache_read(k_cache, nullptr, false, num_pages, page_size, h_kv, slots, tokens, out, out_strides, stream);
+}
+
+int mla_cache_read_fp8(const void *k8, const float *k_scale, int64_t num_pages, int page_size, int h_kv,
+                       const int64_t *slots, int64_t tokens, void *out, const int64_t out_strides[2],
+                       mla_stream_t stream) {
+  return cache_read(k8, k_scale, true, num_pages, page_size, h_kv, slots, tokens, out, out_strides, stream);
+}
+
+int mla_verify_draft(const void *target_probs, const int64_t target_strides[2], const void *draft_probs,
+                     const int64_t draft_strides[2], int dtype, const int32_t *draft_tokens, const float *uniform,
+                     const float *uniform_new, const int32_t *num_drafts, int batch, int drafts, int vocab,
+                     int32_t *accepted, int32_t *tokens, mla_stream_t stream) {
+  if (!target_probs || !target_strides || (draft_probs && !draft_strides) || !draft_tokens || !uniform ||
+      !uniform_new || !accepted || !tokens)
+    return fail(MLA_ERR_ARG, "null pointer argument");
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  if (batch < 1 || batch > (1 << 24) || drafts < 1 || drafts > (1 << 20) || vocab < 1 || vocab > (1 << 30))
+    return fail(MLA_ERR_ARG, "batch must be in [1, 2^24], drafts in [1, 2^20] and vocab in [1, 2^30]");
+  for (int i = 0; i < 2; ++i)
+    if (target_strides[i] < 0 || (draft_probs && draft_strides[i] < 0))
+      return fail(MLA_ERR_ARG, "strides must be non-negative");
+  const size_t size = dtype == MLA_DTYPE_F32 ? 4 : 2;
+  if (!aligned(target_probs, size) || !aligned(draft_probs, size) || !aligned(draft_tokens, 4) ||
+      !aligned(uniform, 4) || !aligned(uniform_new, 4) || !aligned(num_drafts, 4) || !aligned(accepted, 4) ||
+      !aligned(tokens, 4))
+    return fail(MLA_ERR_ARG, "every tensor must be aligned to its element size");
+  VerifyParams p;
+  p.target = target_probs;
+  p.draft = draft_probs;
+  p.t_b = target_strides[0];
+  p.t_s = target_strides[1];
+  p.d_b = draft_probs ? draft_strides[0] : 0;
+  p.d_s = draft_probs ? draft_strides[1] : 0;
+  p.batch = batch;
+  p.drafts = drafts;
+  p.vocab = vocab;
+  p.tokens = draft_tokens;
+  p.uniform = uniform;
+  p.uniform_new = uniform_new;
+  p.num_drafts = num_drafts;
+  p.accepted = accepted;
+  p.out = tokens;
+  cudaError_t e = launch_verify(p, dtype, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "draft verification launch");
   return MLA_OK;
 }
 

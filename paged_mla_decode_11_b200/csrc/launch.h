@@ -5,7 +5,10 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "common.cuh"
+#include "pagedmla.h"
 
 namespace pagedmla {
 
@@ -48,6 +51,67 @@ cudaError_t launch_absorb_q(const __nv_bfloat16 *q_nope, int64_t n_row, int64_t 
                             int H, cudaStream_t stream);
 cudaError_t launch_absorb_out(const __nv_bfloat16 *o_lat, int64_t l_row, int64_t l_head, const __nv_bfloat16 *w_uv,
                               __nv_bfloat16 *out, int T, int H, cudaStream_t stream);
+
+// Rotary positions (rope.cu); strides in elements, the tile sizes are the launcher's.
+struct RopeParams {
+  const void *x;
+  void *out;
+  int64_t x_t, x_h, o_t, o_h;
+  int64_t tokens;
+  int heads, width, pairs;
+  const void *positions;
+  const double *inv_freq;
+  float magnitude;
+  bool pos64, inverse, copy_front;  // copy_front: the columns in front are to be copied (out is not x)
+  int tile_tokens, tile_heads;
+};
+cudaError_t launch_rope(RopeParams p, int dtype, bool half, cudaStream_t stream);
+
+// Cache write and read-back (cache.cu).
+cudaError_t launch_cache_slots(const int32_t *row_ptr, const int32_t *seqlens, int batch, const int32_t *block_table,
+                               int64_t bt_stride, int bt_width, int64_t num_pages, int64_t tokens, int64_t *slots,
+                               int32_t *positions, cudaStream_t stream);
+struct CacheWriteParams {
+  const void *latent, *rope;
+  int64_t l_t, l_h, r_t, r_h;
+  int64_t tokens;
+  int h_kv;
+  const void *weight;       // nullptr: no norm
+  float eps;
+  const void *positions;
+  const double *inv_freq;   // nullptr: rope columns as they are
+  float magnitude;
+  bool pos64, half;
+  const int64_t *slots;
+  void *cache;
+  float *scale;             // nullptr: a bf16 cache
+  int64_t num_slots;
+};
+cudaError_t launch_cache_write(const CacheWriteParams &p, int dtype, cudaStream_t stream);
+struct CacheReadParams {
+  const void *cache;
+  const float *scale;       // nullptr: a bf16 cache
+  int64_t num_slots;
+  int64_t tokens;
+  int h_kv;
+  const int64_t *slots;
+  __nv_bfloat16 *out;
+  int64_t o_t, o_h;
+};
+cudaError_t launch_cache_read(const CacheReadParams &p, cudaStream_t stream);
+
+// Verification of drafted tokens (verify.cu).
+struct VerifyParams {
+  const void *target, *draft;  // draft nullptr: drafts chosen with certainty
+  int64_t t_b, t_s, d_b, d_s;  // element strides of their batch and position dims
+  int batch, drafts, vocab;
+  const int32_t *tokens;
+  const float *uniform, *uniform_new;
+  const int32_t *num_drafts;   // nullptr: all of them
+  int32_t *accepted, *out;
+};
+cudaError_t launch_verify(const VerifyParams &p, int dtype, cudaStream_t stream);
+
 cudaError_t launch_watchdog_selftest(int *status, unsigned long long timeout_ns,
                                      cudaStream_t stream);
 
