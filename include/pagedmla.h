@@ -227,6 +227,25 @@ MLA_API int mla_decode_paged_fp8(const void *q, const int64_t q_strides[3], int 
                                  size_t workspace_bytes, unsigned flags, mla_stream_t stream);
 
 /*
+ * mla_decode_paged_fp8_rows -- mla_decode_paged_fp8 for any number of query rows per latent head
+ * (s_q * h_q / h_kv up to 2^20): up to 16 it is that call, above 16 a CTA-pair tcgen05 kernel whose
+ * products run on the codes themselves.  There the query (per row) and the probabilities times
+ * the key scales are each carried as a sum of two 8-bit terms.  The query's sum is exact for
+ * values down to 2^-10 of the row's largest and within 2^-18 of the largest below; the
+ * probabilities' is within 2^-8 of the value (as a bf16 rounding) or 2^-20 of the row's largest.
+ * k_scale must be finite for every key; a query row that holds an infinity or NaN gives NaN in
+ * its own rows only.  Scales below 2^-100 lose precision.  All arguments, layouts, results and
+ * other errors as in mla_decode_paged_fp8.
+ */
+MLA_API int mla_decode_paged_fp8_rows(const void *q, const int64_t q_strides[3], int batch, int s_q, int h_q,
+                                      int d, const void *k8, const float *k_scale, int64_t num_pages,
+                                      int page_size, int h_kv, const int32_t *block_table,
+                                      int64_t block_table_stride, const int32_t *cache_seqlens, int dv,
+                                      const int32_t *tile_metadata, int num_parts, const int32_t *num_splits,
+                                      float softmax_scale, int causal, void *out, float *lse, void *workspace,
+                                      size_t workspace_bytes, unsigned flags, mla_stream_t stream);
+
+/*
  * mla_get_metadata_csr -- split plan for the token-level sparse decode.  The same balanced
  * cuts as mla_get_metadata, over n_lists key lists (one per query token, n_lists = batch *
  * s_q) whose lengths are row_ptr[i + 1] - row_ptr[i] (row_ptr: device int32 [n_lists + 1]).

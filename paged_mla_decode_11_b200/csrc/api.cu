@@ -250,6 +250,95 @@ int cache_read(const void *cache, const float *k_scale, bool fp8, int64_t num_pa
   return MLA_OK;
 }
 
+// Both FP8 decode entries; any_rows: more than 16 query rows per latent head are taken too.
+int decode_fp8(const void *q, const int64_t *q_strides, int batch, int s_q, int h_q, int d, const void *k8,
+               const float *k_scale, int64_t num_pages, int page_size, int h_kv, const int32_t *block_table,
+               int64_t block_table_stride, const int32_t *cache_seqlens, int dv, const int32_t *tile_metadata,
+               int num_parts, const int32_t *num_splits, float softmax_scale, int causal, void *out, float *lse,
+               void *workspace, size_t workspace_bytes, unsigned flags, mla_stream_t stream, bool any_rows) {
+  if (!q || !q_strides || !k8 || !k_scale || !block_table || !cache_seqlens || !tile_metadata || !num_splits ||
+      !out || !lse)
+    return fail(MLA_ERR_ARG, "null pointer argument");
+  int rc = check_common(batch, s_q, h_q, h_kv, dv);
+  if (rc) return rc;
+  if (d != kD) return fail(MLA_ERR_UNSUPPORTED, "d must be %d (got %d)", kD, d);
+  if (page_size != kPage) return fail(MLA_ERR_UNSUPPORTED, "page_size must be %d (got %d)", kPage, page_size);
+  const int g = h_q / h_kv, R = s_q * g;
+  if (R > 16 && !any_rows)
+    return fail(MLA_ERR_UNSUPPORTED,
+                "this call runs the 16-row kernel: s_q * h_q / h_kv must be <= 16 (got %d); "
+                "mla_decode_paged_fp8_rows takes more", R);
+  if (num_pages < 1 || num_pages > (int64_t(1) << 25))
+    return fail(MLA_ERR_ARG, "num_pages must be in [1, 2^25]");
+  if (block_table_stride < 1) return fail(MLA_ERR_ARG, "block_table_stride must be >= 1");
+  if (num_parts < 1) return fail(MLA_ERR_ARG, "num_parts must be >= 1");
+  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
+    return fail(MLA_ERR_ARG, "softmax_scale must be positive and finite");
+  if (flags & ~MLA_FLAG_SKIP_COMBINE) return fail(MLA_ERR_ARG, "unknown flags 0x%x", flags);
+  for (int i = 0; i < 3; ++i)
+    if (q_strides[i] < 0 || q_strides[i] % 8 != 0)
+      return fail(MLA_ERR_ARG, "q strides must be non-negative multiples of 8 elements");
+  if (!aligned(q, 16) || !aligned(k8, 16) || !aligned(k_scale, 16) || !aligned(out, 16) || !aligned(lse, 4))
+    return fail(MLA_ERR_ARG, "q, k8, k_scale and out must be 16-byte aligned, lse 4-byte aligned");
+  rc = check_device();
+  if (rc) return rc;
+  const WorkspaceLayout wl = workspace_layout(batch, R, h_kv, num_parts);
+  if (!workspace) return fail(MLA_ERR_WORKSPACE, "workspace is null");
+  if (!aligned(workspace, 256)) return fail(MLA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (workspace_bytes < wl.total)
+    return fail(MLA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", workspace_bytes, wl.total);
+
+  CUtensorMap k8_map;
+  rc = encode_k8_map(&k8_map, k8, num_pages, h_kv);
+  if (rc) return rc;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  DecodeParams p;
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.q_sb = q_strides[0];
+  p.q_ss = q_strides[1];
+  p.q_sh = q_strides[2];
+  p.batch = batch;
+  p.s_q = s_q;
+  p.h_q = h_q;
+  p.h_kv = h_kv;
+  p.g = g;
+  p.R = R;
+  p.block_table = block_table;
+  p.bt_stride = block_table_stride;
+  p.kv_base = static_cast<const uint8_t *>(k8);
+  p.kv_token_bytes = int64_t(h_kv) * kD;
+  p.seqlens = cache_seqlens;
+  p.tile_md = tile_metadata;
+  p.num_parts = num_parts;
+  p.num_splits = num_splits;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.causal = causal ? 1 : 0;
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.lse = lse;
+  p.lse_accum = reinterpret_cast<float *>(ws + wl.lse_off);
+  p.o_accum = reinterpret_cast<float *>(ws + wl.o_off);
+  p.status = reinterpret_cast<int *>(ws);
+  p.watchdog_ns = kWatchdogNs;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (R > 16) {
+    e = launch_decode_fp8_pair(k8_map, p, k_scale, num_pages, st);
+  } else {
+    CUtensorMap scale_map, qmap;
+    rc = encode_scale_map(&scale_map, k_scale, num_pages, h_kv);
+    if (rc) return rc;
+    rc = encode_q_map(&qmap, q, batch, s_q, h_q, g, s_q, q_strides);
+    if (rc) return rc;
+    e = launch_decode_fp8(k8_map, scale_map, qmap, p, st);
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "fp8 decode kernel launch");
+  if (!(flags & MLA_FLAG_SKIP_COMBINE)) {
+    e = launch_combine(num_splits, batch, s_q, h_q, h_kv, p.lse_accum, p.o_accum, p.out, lse, st);
+    if (e != cudaSuccess) return cuda_fail(e, "combine kernel launch");
+  }
+  return MLA_OK;
+}
+
 }  // namespace
 
 namespace pagedmla {
@@ -471,80 +560,20 @@ int mla_decode_paged_fp8(const void *q, const int64_t q_strides[3], int batch, i
                          int dv, const int32_t *tile_metadata, int num_parts, const int32_t *num_splits,
                          float softmax_scale, int causal, void *out, float *lse, void *workspace,
                          size_t workspace_bytes, unsigned flags, mla_stream_t stream) {
-  if (!q || !q_strides || !k8 || !k_scale || !block_table || !cache_seqlens || !tile_metadata || !num_splits ||
-      !out || !lse)
-    return fail(MLA_ERR_ARG, "null pointer argument");
-  int rc = check_common(batch, s_q, h_q, h_kv, dv);
-  if (rc) return rc;
-  if (d != kD) return fail(MLA_ERR_UNSUPPORTED, "d must be %d (got %d)", kD, d);
-  if (page_size != kPage) return fail(MLA_ERR_UNSUPPORTED, "page_size must be %d (got %d)", kPage, page_size);
-  const int g = h_q / h_kv, R = s_q * g;
-  if (R > 16)
-    return fail(MLA_ERR_UNSUPPORTED,
-                "the FP8 cache is decoded by the 16-row kernel: s_q * h_q / h_kv must be <= 16 (got %d)", R);
-  if (num_pages < 1 || num_pages > (int64_t(1) << 25))
-    return fail(MLA_ERR_ARG, "num_pages must be in [1, 2^25]");
-  if (block_table_stride < 1) return fail(MLA_ERR_ARG, "block_table_stride must be >= 1");
-  if (num_parts < 1) return fail(MLA_ERR_ARG, "num_parts must be >= 1");
-  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
-    return fail(MLA_ERR_ARG, "softmax_scale must be positive and finite");
-  if (flags & ~MLA_FLAG_SKIP_COMBINE) return fail(MLA_ERR_ARG, "unknown flags 0x%x", flags);
-  for (int i = 0; i < 3; ++i)
-    if (q_strides[i] < 0 || q_strides[i] % 8 != 0)
-      return fail(MLA_ERR_ARG, "q strides must be non-negative multiples of 8 elements");
-  if (!aligned(q, 16) || !aligned(k8, 16) || !aligned(k_scale, 16) || !aligned(out, 16) || !aligned(lse, 4))
-    return fail(MLA_ERR_ARG, "q, k8, k_scale and out must be 16-byte aligned, lse 4-byte aligned");
-  rc = check_device();
-  if (rc) return rc;
-  const WorkspaceLayout wl = workspace_layout(batch, R, h_kv, num_parts);
-  if (!workspace) return fail(MLA_ERR_WORKSPACE, "workspace is null");
-  if (!aligned(workspace, 256)) return fail(MLA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-  if (workspace_bytes < wl.total)
-    return fail(MLA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", workspace_bytes, wl.total);
+  return decode_fp8(q, q_strides, batch, s_q, h_q, d, k8, k_scale, num_pages, page_size, h_kv, block_table,
+                    block_table_stride, cache_seqlens, dv, tile_metadata, num_parts, num_splits, softmax_scale, causal,
+                    out, lse, workspace, workspace_bytes, flags, stream, false);
+}
 
-  CUtensorMap k8_map, scale_map, qmap;
-  rc = encode_k8_map(&k8_map, k8, num_pages, h_kv);
-  if (rc) return rc;
-  rc = encode_scale_map(&scale_map, k_scale, num_pages, h_kv);
-  if (rc) return rc;
-  rc = encode_q_map(&qmap, q, batch, s_q, h_q, g, s_q, q_strides);
-  if (rc) return rc;
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  DecodeParams p;
-  p.q = static_cast<const __nv_bfloat16 *>(q);
-  p.q_sb = q_strides[0];
-  p.q_ss = q_strides[1];
-  p.q_sh = q_strides[2];
-  p.batch = batch;
-  p.s_q = s_q;
-  p.h_q = h_q;
-  p.h_kv = h_kv;
-  p.g = g;
-  p.R = R;
-  p.block_table = block_table;
-  p.bt_stride = block_table_stride;
-  p.kv_base = static_cast<const uint8_t *>(k8);
-  p.kv_token_bytes = int64_t(h_kv) * kD;
-  p.seqlens = cache_seqlens;
-  p.tile_md = tile_metadata;
-  p.num_parts = num_parts;
-  p.num_splits = num_splits;
-  p.scale_log2 = softmax_scale * 1.4426950408889634f;
-  p.causal = causal ? 1 : 0;
-  p.out = static_cast<__nv_bfloat16 *>(out);
-  p.lse = lse;
-  p.lse_accum = reinterpret_cast<float *>(ws + wl.lse_off);
-  p.o_accum = reinterpret_cast<float *>(ws + wl.o_off);
-  p.status = reinterpret_cast<int *>(ws);
-  p.watchdog_ns = kWatchdogNs;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_decode_fp8(k8_map, scale_map, qmap, p, st);
-  if (e != cudaSuccess) return cuda_fail(e, "fp8 decode kernel launch");
-  if (!(flags & MLA_FLAG_SKIP_COMBINE)) {
-    e = launch_combine(num_splits, batch, s_q, h_q, h_kv, p.lse_accum, p.o_accum, p.out, lse, st);
-    if (e != cudaSuccess) return cuda_fail(e, "combine kernel launch");
-  }
-  return MLA_OK;
+int mla_decode_paged_fp8_rows(const void *q, const int64_t q_strides[3], int batch, int s_q, int h_q, int d,
+                              const void *k8, const float *k_scale, int64_t num_pages, int page_size, int h_kv,
+                              const int32_t *block_table, int64_t block_table_stride, const int32_t *cache_seqlens,
+                              int dv, const int32_t *tile_metadata, int num_parts, const int32_t *num_splits,
+                              float softmax_scale, int causal, void *out, float *lse, void *workspace,
+                              size_t workspace_bytes, unsigned flags, mla_stream_t stream) {
+  return decode_fp8(q, q_strides, batch, s_q, h_q, d, k8, k_scale, num_pages, page_size, h_kv, block_table,
+                    block_table_stride, cache_seqlens, dv, tile_metadata, num_parts, num_splits, softmax_scale, causal,
+                    out, lse, workspace, workspace_bytes, flags, stream, true);
 }
 
 int mla_decode_sparse(const void *q, const int64_t q_strides[3], int batch, int s_q, int h_q, int d,

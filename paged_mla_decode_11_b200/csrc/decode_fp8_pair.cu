@@ -1,0 +1,816 @@
+// Paged MLA decode over an FP8 latent cache for more than 16 query rows per latent head, on CTA
+// pairs (tcgen05 cta_group::2, kind::f8f6f4).  Cache format and results as in decode_fp8.cu: the
+// row a token contributes is k_scale * e4m3(code).
+//
+// Both products run on the codes as they are, without widening them, by splitting the other
+// operand into two 8-bit terms whose sum keeps it:
+//   q = 2^-a (q_hi + q_lo)    a the row's own power of two (largest |q| in [128, 256)), q_hi the
+//                             nearest E4M3 value and q_lo, E4M3, the rest.  A bf16 value has 8
+//                             significant bits and E4M3 4: the sum is exact for every |q| above
+//                             2^-10 of the row's largest, below it is off by at most 2^-18 of that
+//   P s 2^(6-e) = v_hi + v_lo  s the key's scale, 2^e above every scale of the piece so far: v_hi the
+//                             nearest E4M3 value, v_lo the rest in E5M2.  For v in [2^k, 2^(k+1)) the
+//                             rest is at most 2^(k-4) and E5M2's half step below that 2^(k-8): within
+//                             2^-8 of the value, as a bf16 rounding of P is, while v >= 2^-6; below,
+//                             within 2^-14, that is 2^-20 of the row's largest
+// so S = (q_hi K^T + q_lo K^T) 2^-a s and O = v_hi V + v_lo V take twice the products at twice the
+// bf16 rate, on half the bytes.  Sums are fp32 in tensor memory.
+//
+// One CTA pair takes 128 query rows (64 per CTA; rows past R are masked).  Per group of two pages
+// (128 keys), as in decode_pair.cu: CTA c of the pair loads page c of the group whole; S has
+// M = 128 rows and N = 128 keys, row r's scores for the first page on lane r of tensor memory and
+// for the second on lane 64 + r.  After the score, CTA 0 holds value columns 0-255 and CTA 1 columns
+// 256-511 of both pages: each loads the partner page's half (an L2 hit) over blocks it no longer
+// needs, at the offsets where its partner keeps the same keys.  O has N = 256 value columns, twice.
+//
+// A page of codes takes 40 KB of shared memory (five blocks of 64 tokens x 128 columns), so three
+// groups fit beside the query instead of the bf16 kernel's two, and three score buffers beside the
+// output in tensor memory: the partner's load and the softmax of a group hide behind the next two
+// groups' scores.
+//
+// Shared memory (per CTA, 8 KB blocks of 64 rows x 128 bytes, 128-byte swizzle):
+//   ring: 3 stages x 6 slots: slots 0-4 the own page's column blocks; after the score CTA 0 reloads
+//         slots 2-3 with the partner page's blocks 0-1 and CTA 1 slots 0-1 with its blocks 2-3; slot
+//         4 (rope, free after the score) takes v_hi and slot 5 v_lo (64 rows x 128 keys)
+//   query: q_hi column blocks 0-3, q_lo blocks 0-3, and one block of both rope halves
+// Tensor memory (512 columns): O (value halves at 0 and 128), S at 256, 320 and 384.
+//
+// Warp roles (both CTAs):
+//   warp 0      producer: own pages and the group's key scales, the partner page's value half
+//   warp 1      tensor-memory owner; in CTA 0 the MMA issuer (one thread)
+//   warps 2-5   softmax, O rescale and epilogue: lane l of sub-partition q owns row (32 q + l) mod 64
+//               and half q / 2 (keys of that page; value columns 256 (q / 2) + 0..255)
+//   warps 6-9   query loaders: 16 rows each, split into q_hi and q_lo
+// Every wait is bounded.
+#include <cuda_fp8.h>
+
+#include "launch.h"
+
+namespace pagedmla {
+
+namespace {
+
+struct FpPair {
+  static constexpr int kThreads = 320;
+  static constexpr int BM = 64;                  // query rows per CTA
+  static constexpr int kStages = 3;
+  static constexpr int kBlock = 64 * 128;        // bytes of a block
+  static constexpr int kPageBlocks = 5;          // column blocks of a page (the last one half filled)
+  static constexpr int kSlots = kPageBlocks + 1;
+  static constexpr int kQScales = 8;             // row-scale buffers, by piece
+  static constexpr int kOffRing = 0;
+  static constexpr int kOffQ = kOffRing + kStages * kSlots * kBlock;
+  static constexpr int kOffX = kOffQ + 9 * kBlock;            // row-max exchange [2][2][64], row sums [2][64]
+  static constexpr int kOffSc = kOffX + (4 + 2) * 64 * 4;     // key scales [stage][128]
+  static constexpr int kOffQSc = kOffSc + kStages * 128 * 4;  // row scales [8][64]
+  enum {
+    FULL = 0, VFULL = FULL + kStages, EMPTY = VFULL + kStages, SFULL = EMPTY + kStages, SFREE = SFULL + kStages,
+    PFULL = SFREE + kStages, SCALES = PFULL + kStages, QSC = SCALES + kStages, OFULL = QSC + kQScales,
+    OFREE = OFULL + 1, QFULL = OFREE + 1, QFREE = QFULL + 1, FINAL = QFREE + 1, NBARS = FINAL + 1
+  };
+  static constexpr int kOffBar = kOffQSc + kQScales * 64 * 4;
+  static constexpr int kOffTmem = kOffBar + NBARS * 8;
+  static constexpr int kOffAbort = kOffTmem + 8;
+  static constexpr int kSmemBytes = kOffAbort + 8 + 1024;     // + slack for 1 KB alignment
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kTmemO = 0;          // value halves v at 128 v
+  static constexpr uint32_t kTmemS = 256;        // score buffers at 256 + 64 stage
+  static constexpr uint32_t kOwnBytes = kPageBlocks * kBlock;  // a page (its last block's fill counts)
+  static constexpr uint32_t kHalfVBytes = 2 * kBlock;          // half of a page's values
+  static_assert(kOffQ % 1024 == 0, "swizzled tiles need 1 KB alignment");
+  static_assert(kTmemS + 64 * kStages <= kTmemCols, "tensor memory");
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+// ------------------------------------------------------------------------------------
+// CTA-pair helpers.
+// ------------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Cluster address of the same shared-memory offset in CTA 0 of the pair.
+__device__ __forceinline__ uint32_t map_cta0(uint32_t local) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(local));
+  return r;
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// TMA load into this CTA's shared memory, its bytes counted on a barrier of CTA 0.
+__device__ __forceinline__ void load_for_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar_cluster, int c0, int c1,
+                                              int c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f8f6f4 with fp32 D and E4M3 B; A is E4M3, or E5M2 (a_e5m2).
+__device__ constexpr uint32_t idesc_f8(int M, int N, bool a_e5m2, bool b_mn_major) {
+  return (1u << 4) | (uint32_t(a_e5m2) << 7) | (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) |
+         (uint32_t(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Arrive once on the barrier at this offset in both CTAs when all tcgen05 work issued so far by
+// this thread is done.
+__device__ __forceinline__ void commit_both(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t taddr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+      "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+      "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+      : "memory");
+}
+
+__device__ __forceinline__ bool all_lanes(bool v) { return __all_sync(0xffffffffu, v); }
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
+
+// Two values as 8-bit codes (low byte first), and the rest of E4M3 codes' values.
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t to_e5m2x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(codes), __NV_E4M3)));
+}
+
+// ------------------------------------------------------------------------------------
+// Pieces of a part and their groups of two pages.
+// ------------------------------------------------------------------------------------
+struct Piece {
+  int L, t0, t1, ntiles, ngroups;  // the last group may hold one page
+};
+
+// One sequence piece of a part, trimmed to the keys the pair's 128 rows can see.
+__device__ __forceinline__ Piece piece_of(const DecodeParams &p, const PartCursor &pc, int seq, int prow0) {
+  Piece w;
+  w.L = p.seqlens[seq];
+  w.t0 = seq == pc.bi ? pc.bt : 0;
+  w.t1 = seq == pc.ei ? pc.et : w.L;
+  if (p.causal) {
+    const int last_row = min(p.R - 1, prow0 + 2 * FpPair::BM - 1);
+    w.t1 = min(w.t1, w.L - (p.s_q - 1 - last_row / p.g));
+  }
+  w.ntiles = w.t1 > w.t0 ? (w.t1 - w.t0 + kPage - 1) / kPage : 0;
+  w.ngroups = (w.ntiles + 1) / 2;
+  return w;
+}
+
+// Walks a part's groups in order, with its stage of the ring and that stage's phase.
+struct Groups {
+  int seq, j, ntiles, ngroups, t0;
+  int count, stage, phase;
+  bool done;
+
+  __device__ __forceinline__ void seek(const DecodeParams &p, const PartCursor &pc, int prow0, int from) {
+    for (seq = from; part_has(pc, seq); ++seq) {
+      const Piece w = piece_of(p, pc, seq, prow0);
+      if (w.ngroups > 0) {
+        j = 0;
+        ntiles = w.ntiles;
+        ngroups = w.ngroups;
+        t0 = w.t0;
+        done = false;
+        return;
+      }
+    }
+    done = true;
+  }
+  __device__ __forceinline__ void start(const DecodeParams &p, const PartCursor &pc, int prow0) {
+    count = stage = phase = 0;
+    seek(p, pc, prow0, pc.bi);
+  }
+  __device__ __forceinline__ void next(const DecodeParams &p, const PartCursor &pc, int prow0) {
+    ++count;
+    if (++stage == FpPair::kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+    if (++j == ngroups) seek(p, pc, prow0, seq + 1);
+  }
+  // The group's two pages; a lone last page stands for both (its second half is masked).
+  __device__ __forceinline__ void pages(const DecodeParams &p, int &a, int &b) const {
+    const int32_t *row = p.block_table + int64_t(seq) * p.bt_stride + t0 / kPage;
+    a = row[2 * j];
+    b = row[min(2 * j + 1, ntiles - 1)];
+  }
+};
+
+}  // namespace
+
+// The pair is the cluster's x dimension (grid x = the CTAs of the 128-row blocks, y = parts, z =
+// latent heads).
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
+    decode_fp8_pair_kernel(const __grid_constant__ CUtensorMap k8_map, const DecodeParams p,
+                           const float *__restrict__ k_scale, int64_t scale_head) {
+  using T = FpPair;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rank = int(cta_rank());
+  const int part = blockIdx.y, kvh = blockIdx.z;
+  const int prow0 = int(blockIdx.x / 2) * 2 * T::BM;  // first row of the pair's 128-row block
+  const int crow0 = prow0 + rank * T::BM;             // first row of this CTA
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + T::kOffBar;
+  auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
+  auto bar_cta0 = [&](int i) { return map_cta0(bar(i)); };  // barriers both CTAs arrive on live in CTA 0
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + T::kOffAbort);
+  const uint32_t sQ = sbase + T::kOffQ;
+  auto slot = [&](int st, int k) { return sbase + uint32_t(T::kOffRing + (st * T::kSlots + k) * T::kBlock); };
+  float *xmax = reinterpret_cast<float *>(smem + T::kOffX);  // [2 parity][2 half][64 rows]
+  float *xsum = xmax + 4 * 64;                                // [2 half][64 rows]
+  float *qscale = reinterpret_cast<float *>(smem + T::kOffQSc);
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < T::kStages; ++i) {
+      mbar_init(bar(T::FULL + i), 1);
+      mbar_init(bar(T::VFULL + i), 1);
+      mbar_init(bar(T::EMPTY + i), 1);
+      mbar_init(bar(T::SFULL + i), 1);
+      mbar_init(bar(T::SFREE + i), 8);
+      mbar_init(bar(T::PFULL + i), 8);
+      mbar_init(bar(T::SCALES + i), 1);
+    }
+    for (int i = 0; i < T::kQScales; ++i) mbar_init(bar(T::QSC + i), 4);
+    mbar_init(bar(T::OFULL), 1);
+    mbar_init(bar(T::OFREE), 8);
+    mbar_init(bar(T::QFULL), 8);
+    mbar_init(bar(T::QFREE), 1);
+    mbar_init(bar(T::FINAL), 1);
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sbase + T::kOffTmem),
+                 "r"(T::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  pair_sync();  // both CTAs' barriers are initialised before any cross-CTA arrive
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + T::kOffTmem);
+  grid_dependency_wait();  // the plan comes from the scheduler kernel just before
+  const PartCursor pc = load_part(p.tile_md, part);
+  const unsigned long long lim_ns = p.watchdog_ns;
+
+  if (warp == 0) {
+    // ------------------------- producer (one thread in both CTAs) -------------------------
+    if (lane == 0) {
+      prefetch_tensormap(&k8_map);
+      // pages are read by both CTAs of the pair (the second time from L2)
+      const uint64_t policy = l2_evict_normal_policy();
+      const float *scales = k_scale + int64_t(kvh) * scale_head;
+      const bool prefetch = p.h_kv == 1;
+      Groups wa, wb, wf;  // own pages, partner value halves, L2 prefetch ahead of the own pages
+      wa.start(p, pc, prow0);
+      wb = wa;
+      wf = wa;
+      if (prefetch)
+        for (int i = 0; i < T::kStages && !wf.done; ++i) wf.next(p, pc, prow0);
+      bool ok = true;
+      unsigned long long idle_since = 0;
+      uint32_t spins = 0;
+      while (ok && (!wa.done || wb.count < wa.count)) {
+        bool progressed = false;
+        // the partner page's value half of a group, once its score is done
+        if (wb.count < wa.count && mbar_test_wait(bar(T::SFULL + wb.stage), wb.phase)) {
+          int pa, pb;
+          wb.pages(p, pa, pb);
+          const int phys = leader ? pb : pa;
+          if (leader) mbar_arrive_expect_tx(bar(T::VFULL + wb.stage), 2 * T::kHalfVBytes);
+          for (int c = 0; c < 2; ++c)
+            load_for_pair(slot(wb.stage, leader ? 2 + c : c), &k8_map, bar_cta0(T::VFULL + wb.stage),
+                          (leader ? c : 2 + c) * 128, kvh, phys * kPage, policy);
+          wb.next(p, pc, prow0);
+          progressed = true;
+        }
+        // the own page and the scales of a group, once the products of the stage's last group are done
+        if (!progressed && !wa.done &&
+            (wa.count < T::kStages || mbar_test_wait(bar(T::EMPTY + wa.stage), wa.phase ^ 1))) {
+          int pa, pb;
+          wa.pages(p, pa, pb);
+          const int phys = leader ? pa : pb, st = wa.stage;
+          if (leader) mbar_arrive_expect_tx(bar(T::FULL + st), 2 * T::kOwnBytes);
+          const uint32_t fb = bar_cta0(T::FULL + st);
+#pragma unroll
+          for (int c = 0; c < T::kPageBlocks; ++c) load_for_pair(slot(st, c), &k8_map, fb, c * 128, kvh, phys * kPage, policy);
+          const uint32_t sc = sbase + T::kOffSc + st * 512;
+          mbar_arrive_expect_tx(bar(T::SCALES + st), 512);
+          bulk_load_hint(sc, scales + int64_t(pa) * kPage, 256, bar(T::SCALES + st), policy);
+          bulk_load_hint(sc + 256, scales + int64_t(pb) * kPage, 256, bar(T::SCALES + st), policy);
+          if (prefetch && !wf.done) {
+            int fa, fb2;
+            wf.pages(p, fa, fb2);
+            prefetch_l2_bulk(p.kv_base + int64_t(leader ? fa : fb2) * kPage * p.kv_token_bytes, kPage * kD);
+            wf.next(p, pc, prow0);
+          }
+          wa.next(p, pc, prow0);
+          progressed = true;
+        }
+        if (progressed) {
+          idle_since = 0;
+        } else if (__nanosleep(32), (++spins & 15u) == 0) {
+          const unsigned long long now = global_ns();
+          if (*abort) {
+            ok = false;
+          } else if (idle_since == 0) {
+            idle_since = now;
+          } else if (now - idle_since > lim_ns) {
+            *abort = 1;
+            report_timeout(p.status);
+            ok = false;
+          }
+        }
+      }
+      // Every copy issued lands before the CTAs exit: the scales on this CTA's barriers, the pages
+      // of both CTAs on CTA 0's (CTA 1 leaves after CTA 0: the final cluster barrier).  The last
+      // group of each stage is the one to wait for.
+      int never = 0;
+      for (int i = 1; i <= T::kStages; ++i) {
+        const int ga = wa.count - i, gb = wb.count - i;
+        if (ga >= 0) {
+          mbar_wait(bar(T::SCALES + ga % T::kStages), (ga / T::kStages) & 1, &never, p.status, lim_ns);
+          if (leader) mbar_wait(bar(T::FULL + ga % T::kStages), (ga / T::kStages) & 1, &never, p.status, lim_ns);
+        }
+        if (leader && gb >= 0) mbar_wait(bar(T::VFULL + gb % T::kStages), (gb / T::kStages) & 1, &never, p.status, lim_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (leader && lane == 0) {
+      // ------------------------- MMA issuer (CTA 0, one thread) -------------------------
+      // The score of a group needs its pages in both CTAs (FULL), the query tile (QFULL) and its
+      // score buffer read (SFREE); its PV needs both CTAs' v tiles (PFULL) and partner halves
+      // (VFULL), and at a piece's first group the previous epilogue (OFREE).  Scores run at most
+      // kStages groups ahead of PV, and PV goes first when both are ready.
+      const uint32_t idesc_qk = idesc_f8(128, 128, false, false);
+      const uint32_t idesc_hi = idesc_f8(128, 256, false, true), idesc_lo = idesc_f8(128, 256, true, true);
+      Groups wq, wv;
+      wq.start(p, pc, prow0);
+      wv = wq;
+      int qpiece = 0, vpiece = 0;
+      bool have_q = false, ok = true;
+      unsigned long long idle_since = 0;
+      uint32_t spins = 0;
+      while (ok && !wv.done) {
+        bool progressed = false;
+        if (wv.count < wq.count) {
+          const int st = wv.stage;
+          const bool first = wv.j == 0;
+          if (mbar_test_wait(bar(T::PFULL + st), wv.phase) && mbar_test_wait(bar(T::VFULL + st), wv.phase) &&
+              (!first || vpiece == 0 || mbar_test_wait(bar(T::OFREE), (vpiece - 1) & 1))) {
+            tc_fence_after();
+            // a lone last page: the second page's keys are masked (v = 0), skip their products
+            const int halves = (2 * wv.j + 1 < wv.ntiles) ? 2 : 1;
+            // descriptors step by (byte offset >> 4) in their address field
+            const uint64_t hi = smem_desc_sw128(slot(st, 4), 16, 1024), lo = smem_desc_sw128(slot(st, 5), 16, 1024);
+            const uint64_t vb = smem_desc_sw128(slot(st, 0), T::kBlock, 1024);
+            for (int h = 0; h < halves; ++h)
+#pragma unroll
+              for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                  const uint64_t a = uint64_t((h * 64 + ks * 32) >> 4);
+                  const uint64_t b = vb + uint64_t(((2 * h + v) * T::kBlock + ks * 4096) >> 4);
+                  mma_f8_pair(tmem + T::kTmemO + 128 * v, hi + a, b, idesc_hi, (!first || h > 0 || ks > 0) ? 1u : 0u);
+                  mma_f8_pair(tmem + T::kTmemO + 128 * v, lo + a, b, idesc_lo, 1u);
+                }
+            commit_both(bar(T::EMPTY + st));
+            if (wv.j + 1 == wv.ngroups) {
+              commit_both(bar(T::OFULL));
+              ++vpiece;
+            }
+            wv.next(p, pc, prow0);
+            progressed = true;
+          }
+        }
+        if (!progressed && !wq.done && wq.count < wv.count + T::kStages) {
+          const int st = wq.stage;
+          if (!have_q) have_q = mbar_test_wait(bar(T::QFULL), qpiece & 1);
+          if (have_q && mbar_test_wait(bar(T::FULL + st), wq.phase) &&
+              (wq.count < T::kStages || mbar_test_wait(bar(T::SFREE + st), wq.phase ^ 1))) {
+            tc_fence_after();
+            const uint32_t d = tmem + T::kTmemS + 64 * st;
+            const uint64_t kb = smem_desc_sw128(slot(st, 0), 16, 1024), qa = smem_desc_sw128(sQ, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < kD / 32; ++kk) {
+              const int cb = kk >> 2, in = (kk & 3) * 32;
+              const uint64_t b = kb + uint64_t((cb * T::kBlock + in) >> 4);
+              const uint64_t hi = uint64_t((cb < 4 ? cb * T::kBlock + in : 8 * T::kBlock + in) >> 4);
+              const uint64_t lo = uint64_t((cb < 4 ? (4 + cb) * T::kBlock + in : 8 * T::kBlock + 64 + in) >> 4);
+              mma_f8_pair(d, qa + hi, b, idesc_qk, kk > 0 ? 1u : 0u);
+              mma_f8_pair(d, qa + lo, b, idesc_qk, 1u);
+            }
+            commit_both(bar(T::SFULL + st));
+            if (wq.j + 1 == wq.ngroups) {
+              commit_both(bar(T::QFREE));  // the query tile may be replaced
+              have_q = false;
+              ++qpiece;
+            }
+            wq.next(p, pc, prow0);
+            progressed = true;
+          }
+        }
+        if (progressed) {
+          idle_since = 0;
+        } else if (__nanosleep(32), (++spins & 15u) == 0) {
+          const unsigned long long now = global_ns();
+          if (*abort) {
+            ok = false;
+          } else if (idle_since == 0) {
+            idle_since = now;
+          } else if (now - idle_since > lim_ns) {
+            *abort = 1;
+            report_timeout(p.status);
+            ok = false;
+          }
+        }
+      }
+      commit_both(bar(T::FINAL));
+    }
+    __syncwarp();
+    // all tensor-core work (issued by CTA 0, writing both CTAs' tensor memory) is complete before
+    // either CTA releases its tensor memory
+    if (lane == 0) {
+      int never = 0;
+      mbar_wait(bar(T::FINAL), 0, &never, p.status, lim_ns);
+    }
+    __syncwarp();
+  } else if (warp < 6) {
+    // ------------------------- softmax / O rescale / epilogue -------------------------
+    const int q = warp & 3;                 // tensor-memory sub-partition of this warp
+    const int lrow = (32 * q + lane) & 63;  // row within the CTA's 64
+    const int hf = q >> 1;                  // 0: first page's keys, values 0-255; 1: second page, 256-511
+    const int row = crow0 + lrow;
+    const bool active = row < p.R;
+    const int s_row = row / p.g, h_row = kvh * p.g + row % p.g;
+    const uint32_t lanes = tmem + (uint32_t(32 * q) << 16);
+    const int xbar = 1 + (q & 1);           // named barrier of the two warps sharing rows
+    const uint32_t sfree = bar_cta0(T::SFREE), pfull = bar_cta0(T::PFULL), ofree = bar_cta0(T::OFREE);
+    int g = 0, st = 0, phase = 0, last_st = 0, last_phase = 0, qs = 0;
+    bool ok = true;
+    for (int seq = pc.bi; part_has(pc, seq); ++seq) {
+      const Piece w = piece_of(p, pc, seq, prow0);
+      const int ns0 = split_base(p.num_splits, seq);
+      const int nsplit = split_base(p.num_splits, seq + 1) - ns0;
+      const int ord = seq == pc.bi ? pc.bord : 0;
+      const int64_t acc_row = (int64_t(ns0 + ord) * p.h_kv + kvh) * p.R + row;
+      __nv_bfloat16 *out_row = p.out + ((int64_t(seq) * p.s_q + s_row) * p.h_q + h_row) * kDV + hf * 256;
+      float *lse_row = p.lse + (int64_t(seq) * p.h_q + h_row) * p.s_q + s_row;
+      if (w.ngroups == 0) {
+        // no visible key in this piece: zero output (or partial) and lse = -inf
+        if (active) {
+          if (nsplit == 1) {
+            for (int i = 0; i < 32; ++i) reinterpret_cast<uint4 *>(out_row)[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (hf == 0) *lse_row = -INFINITY;
+          } else {
+            float4 *o = reinterpret_cast<float4 *>(p.o_accum + acc_row * kDV + hf * 256);
+            for (int i = 0; i < 64; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (hf == 0) p.lse_accum[acc_row] = -INFINITY;
+          }
+        }
+        continue;
+      }
+      // rows past R and rows without a visible key get v = 0 (every key masked)
+      const int lim = active ? min(w.t1, p.causal ? w.L - (p.s_q - 1 - s_row) : w.L) : -1;
+      ok = all_lanes(ok && mbar_wait(bar(T::QSC + (qs & (T::kQScales - 1))), (qs / T::kQScales) & 1, abort, p.status, lim_ns));
+      // score of raw products to log2 units: 2^-a of the row and the softmax scale
+      // (kept above 0, so that a masked score stays -inf)
+      const float rowf = fmaxf(qscale[(qs & (T::kQScales - 1)) * 64 + lrow] * p.scale_log2, 1.2e-38f);
+      float m_used = -INFINITY, l = 0.f;  // l: this thread's half of the row sum
+      int e_used = -100;                  // every key scale of the piece so far is below 2^e_used
+      for (int j = 0; j < w.ngroups; ++j, ++g) {
+        ok = all_lanes(ok && mbar_wait(bar(T::SFULL + st), phase, abort, p.status, lim_ns));
+        ok = all_lanes(ok && mbar_wait(bar(T::SCALES + st), phase, abort, p.status, lim_ns));
+        tc_fence_after();
+        float sv[64];
+        if (ok) {
+          float t[32];
+          tmem_ld32(lanes + T::kTmemS + 64 * st, t);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sv[i] = t[i];
+          tmem_ld32(lanes + T::kTmemS + 64 * st + 32, t);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sv[32 + i] = t[i];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(sfree + 8u * st);
+        const float4 *sc4 = reinterpret_cast<const float4 *>(smem + T::kOffSc + st * 512);
+        const int group0 = w.t0 + 128 * j, key0 = group0 + 64 * hf;
+        // the largest scale of the group's keys, the same in every thread of the pair; slots past the
+        // piece's end are not keys and their scales are never used
+        const float4 mine = sc4[lane];
+        const int left = w.t1 - (group0 + 4 * lane);
+        uint32_t sb = 0;
+        if (left > 0) sb = __float_as_uint(fabsf(mine.x));
+        if (left > 1) sb = max(sb, __float_as_uint(fabsf(mine.y)));
+        if (left > 2) sb = max(sb, __float_as_uint(fabsf(mine.z)));
+        if (left > 3) sb = max(sb, __float_as_uint(fabsf(mine.w)));
+        const int e_new = max(e_used, int(__reduce_max_sync(0xffffffffu, sb) >> 23) - 126);
+        const bool partial = key0 + 64 > lim;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 s = sc4[16 * hf + i];
+          sv[4 * i] *= s.x;
+          sv[4 * i + 1] *= s.y;
+          sv[4 * i + 2] *= s.z;
+          sv[4 * i + 3] *= s.w;
+        }
+        // keys at or past this row's limit get -inf (only partial groups need the test)
+        if (partial) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (key0 + i >= lim) sv[i] = -INFINITY;
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rowf;
+        // the row's other half lives on the partner warp: exchange maxima
+        xmax[((g & 1) * 2 + hf) * 64 + lrow] = mx;
+        named_bar_sync(xbar, 64);
+        mx = fmaxf(mx, xmax[((g & 1) * 2 + (hf ^ 1)) * 64 + lrow]);
+        // The running maximum is refreshed when it grows by more than 2 (log2 units), so P stays
+        // below 4 and v = P s 2^(6-e) below 256, inside E4M3
+        const float m_new = fmaxf(m_used, mx);
+        const bool need = m_new > m_used + 2.f;
+        float alpha = 1.f;
+        if (need) {
+          alpha = fast_exp2(m_used - m_new);
+          m_used = m_new;
+        }
+        const float nbase = m_used == -INFINITY ? 0.f : -m_used;
+        l *= alpha;
+        const bool rescale = j > 0 && (__any_sync(0xffffffffu, need) || e_new > e_used);
+        alpha *= e_new - e_used < 127 ? pow2(-min(e_new - e_used, 126)) : 0.f;
+        e_used = e_new;
+        const float f = pow2(6 - e_used);
+        uint32_t hi[16], lo[16];
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 s = sc4[16 * hf + i];
+          float v[4];
+          const float ks[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float e = fast_exp2(fmaf(sv[4 * i + k], rowf, nbase));
+            s4[k] += e;
+            v[k] = e * (ks[k] * f);
+            if (partial && key0 + 4 * i + k >= lim) v[k] = 0.f;
+          }
+          const uint32_t h0 = to_e4m3x2(v[0], v[1]), h1 = to_e4m3x2(v[2], v[3]);
+          const float2 b0 = from_e4m3x2(h0), b1 = from_e4m3x2(h1);
+          hi[i] = h0 | h1 << 16;
+          lo[i] = to_e5m2x2(v[0] - b0.x, v[1] - b0.y) | to_e5m2x2(v[2] - b1.x, v[3] - b1.y) << 16;
+        }
+        l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        // O may be rescaled once the previous group's PV has completed (its commit arrives on EMPTY
+        // of that group's stage; that barrier is at most one phase behind)
+        if (rescale) {
+          ok = all_lanes(ok && mbar_wait(bar(T::EMPTY + last_st), last_phase, abort, p.status, lim_ns));
+          if (ok) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < 256; c0 += 32) {
+              float v[32];
+              tmem_ld32(lanes + T::kTmemO + c0, v);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] *= alpha;
+              tmem_store32(lanes + T::kTmemO + c0, v);
+            }
+            tmem_st_wait();
+          }
+        }
+        if (ok) {
+          // the two terms of v into their tiles: 64 keys are four 16-byte chunks of a row
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot(st, 4) + sw128(lrow, 4 * hf + c)),
+                         "r"(hi[4 * c]), "r"(hi[4 * c + 1]), "r"(hi[4 * c + 2]), "r"(hi[4 * c + 3])
+                         : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot(st, 5) + sw128(lrow, 4 * hf + c)),
+                         "r"(lo[4 * c]), "r"(lo[4 * c + 1]), "r"(lo[4 * c + 2]), "r"(lo[4 * c + 3])
+                         : "memory");
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(pfull + 8u * st);
+        last_st = st;
+        last_phase = phase;
+        if (++st == T::kStages) {
+          st = 0;
+          phase ^= 1;
+        }
+      }
+
+      // ---- epilogue: O / l -> output (or fp32 split partial), natural-log LSE ----
+      xsum[hf * 64 + lrow] = l;
+      named_bar_sync(xbar, 64);
+      const float l_row = l + xsum[(hf ^ 1) * 64 + lrow];
+      ok = all_lanes(ok && mbar_wait(bar(T::OFULL), qs & 1, abort, p.status, lim_ns));
+      tc_fence_after();
+      if (ok) {
+        const float inv = l_row > 0.f ? pow2(e_used - 6) / l_row : (l_row == 0.f ? 0.f : l_row);
+        for (int c0 = 0; c0 < 256; c0 += 32) {
+          float v[32];
+          tmem_ld32(lanes + T::kTmemO + c0, v);
+          if (!active) continue;
+          if (nsplit == 1) {
+            uint4 *o = reinterpret_cast<uint4 *>(out_row + c0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              o[k] = make_uint4(pack_bf16x2(v[8 * k] * inv, v[8 * k + 1] * inv),
+                                pack_bf16x2(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
+                                pack_bf16x2(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
+                                pack_bf16x2(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
+          } else {
+            float4 *o = reinterpret_cast<float4 *>(p.o_accum + acc_row * kDV + hf * 256 + c0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              o[k] = make_float4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
+          }
+        }
+        if (active && hf == 0) {
+          const float lse_v = l_row == 0.f ? -INFINITY : (m_used + fast_log2(l_row)) * 0.69314718055994531f;
+          if (nsplit == 1)
+            *lse_row = lse_v;
+          else
+            // a maximum over partials would pass over a NaN; +inf makes the merged row NaN
+            p.lse_accum[acc_row] = lse_v == lse_v ? lse_v : INFINITY;
+        }
+      }
+      tc_fence_before();
+      // the row-sum slots are rewritten by the next piece only after both warps have read them
+      named_bar_sync(xbar, 64);
+      if (lane == 0) arrive_cluster(ofree);
+      ++qs;
+    }
+  } else {
+    // ------------------------- query loaders -------------------------
+    // A warp takes 16 rows: lane l holds 16-byte chunks l and l + 32 (8 columns each) of every row,
+    // and of the rope columns (chunks 64-71) those of rows l / 8 + 4 i.  Read and split into codes
+    // before the previous piece's query tile is free, then stored.
+    const int wq = warp - 6, row0 = wq * 16;
+    const int my_row = crow0 + row0 + (lane & 15);
+    const bool my_active = my_row < p.R;
+    const int64_t my_off = int64_t(my_row / p.g) * p.q_ss + int64_t(kvh * p.g + my_row % p.g) * p.q_sh;
+    const uint32_t qfull = bar_cta0(T::QFULL);
+    int qs = 0;
+    bool ok = true;
+    for (int seq = pc.bi; part_has(pc, seq); ++seq) {
+      if (piece_of(p, pc, seq, prow0).ngroups == 0) continue;
+      const __nv_bfloat16 *base = p.q + int64_t(seq) * p.q_sb;
+      uint4 a[16][2], r[4];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool on = __shfl_sync(0xffffffffu, int(my_active), i) != 0;
+        const uint4 *src = reinterpret_cast<const uint4 *>(base + __shfl_sync(0xffffffffu, my_off, i));
+        a[i][0] = on ? __ldcg(src + lane) : make_uint4(0u, 0u, 0u, 0u);
+        a[i][1] = on ? __ldcg(src + lane + 32) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int x = lane / 8 + 4 * i;
+        const bool on = __shfl_sync(0xffffffffu, int(my_active), x) != 0;
+        const uint4 *src = reinterpret_cast<const uint4 *>(base + __shfl_sync(0xffffffffu, my_off, x));
+        r[i] = on ? __ldcg(src + 64 + lane % 8) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      // largest magnitude of eight bf16 values, as its bits (non-negative values order as integers)
+      auto top = [](const uint4 &u) {
+        const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = max(m, max(w4[k] & 0x7fffu, (w4[k] >> 16) & 0x7fffu));
+        return m;
+      };
+      // eight bf16 values times `up` as E4M3 codes (x, y) and the codes of the rest (z, w)
+      auto split = [](const uint4 &u, float up) {
+        const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+        uint32_t h[4], lw[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w4[k]));
+          const float x = f.x * up, y = f.y * up;
+          h[k] = to_e4m3x2(x, y);
+          const float2 b = from_e4m3x2(h[k]);
+          lw[k] = to_e4m3x2(x - b.x, y - b.y);
+        }
+        return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, lw[0] | lw[1] << 16, lw[2] | lw[3] << 16);
+      };
+      uint32_t rope_top[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t m = top(r[i]);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        rope_top[i] = m;
+      }
+      int my_e = 0;  // biased exponent of row (lane & 15)'s largest value
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, max(top(a[i][0]), top(a[i][1])));
+        const int e = max(int(max(m, __shfl_sync(0xffffffffu, rope_top[i / 4], (i % 4) * 8)) >> 7), 8);
+        // 2^(7 - (e - 127)); a row with an infinity or NaN becomes NaN
+        const float up = e == 255 ? __int_as_float(0x7fffffff) : pow2(134 - e);
+        a[i][0] = split(a[i][0], up);
+        a[i][1] = split(a[i][1], up);
+        if ((lane & 15) == i) my_e = e;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = __shfl_sync(0xffffffffu, my_e, lane / 8 + 4 * i);
+        r[i] = split(r[i], e == 255 ? __int_as_float(0x7fffffff) : pow2(134 - e));
+      }
+      if (qs > 0) ok = all_lanes(ok && mbar_wait(bar(T::QFREE), (qs - 1) & 1, abort, p.status, lim_ns));
+      if (ok) {
+        auto put = [&](int block, int x, int byte, uint32_t u, uint32_t v) {
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sQ + block * T::kBlock + sw128(x, byte >> 4) + (byte & 8)),
+                       "r"(u), "r"(v)
+                       : "memory");
+        };
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int col = 8 * (lane + 32 * c);
+            put(col / 128, row0 + i, col % 128, a[i][c].x, a[i][c].y);
+            put(4 + col / 128, row0 + i, col % 128, a[i][c].z, a[i][c].w);
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int x = row0 + lane / 8 + 4 * i, byte = 8 * (lane % 8);
+          put(8, x, byte, r[i].x, r[i].y);
+          put(8, x, 64 + byte, r[i].z, r[i].w);
+        }
+        if (lane < 16)
+          qscale[(qs & (T::kQScales - 1)) * 64 + row0 + lane] = my_e == 255 ? __int_as_float(0x7fffffff) : pow2(my_e - 134);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(T::QSC + (qs & (T::kQScales - 1))));
+        arrive_cluster(qfull);
+      }
+      ++qs;
+    }
+  }
+  grid_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  pair_sync();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(T::kTmemCols) : "memory");
+  pair_sync();
+}
+
+cudaError_t launch_decode_fp8_pair(const CUtensorMap &k8_map, const DecodeParams &p, const float *k_scale,
+                                   int64_t num_pages, cudaStream_t stream) {
+  using T = FpPair;
+  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_fp8_pair_kernel), T::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const unsigned pairs = unsigned((p.R + 2 * T::BM - 1) / (2 * T::BM));
+  return launch_early(decode_fp8_pair_kernel, dim3(2 * pairs, p.num_parts, p.h_kv), dim3(T::kThreads), T::kSmemBytes,
+                      stream, k8_map, p, k_scale, num_pages * kPage);
+}
+
+}  // namespace pagedmla

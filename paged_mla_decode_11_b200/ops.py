@@ -44,7 +44,7 @@ EXPORTED = (
     "mla_last_error_string", "mla_decode_paged_static", "mla_query_status_static", "mla_decode_paged_fp8",
     "mla_merge_partials", "mla_absorb_query", "mla_absorb_output", "mla_get_metadata_csr", "mla_decode_sparse",
     "mla_rope", "mla_cache_slots", "mla_cache_write", "mla_cache_write_fp8", "mla_cache_read", "mla_cache_read_fp8",
-    "mla_verify_draft",
+    "mla_verify_draft", "mla_decode_paged_fp8_rows",
 )
 MLA_ROPE_HALF = 1
 MLA_ROPE_INVERSE = 2
@@ -95,6 +95,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "mla_get_metadata_csr": [P, I, I, I, P, P, P],
             "mla_decode_sparse": [P, P, I, I, I, I, P, I64, I, I, P, I64, P, P, P, I, P, I, P,
                                   ctypes.c_float, I, P, P, P, ctypes.c_size_t, ctypes.c_uint, P],
+            "mla_decode_paged_fp8_rows": [P, P, I, I, I, I, P, P, I64, I, I, P, I64, P, I, P, I, P,
+                                          ctypes.c_float, I, P, P, P, ctypes.c_size_t, ctypes.c_uint, P],
             "mla_rope": [P, P, I, I64, I, I, I, P, P, ctypes.c_float, ctypes.c_uint, P, P, P],
             "mla_cache_slots": [P, P, I, P, I64, I, I64, I64, P, P, P],
             "mla_cache_write": [P, P, P, P, I, I64, I, P, ctypes.c_float, P, P, ctypes.c_float, ctypes.c_uint, P, P,
@@ -339,6 +341,24 @@ def mla_decode_paged_fp8(q: torch.Tensor, k8: torch.Tensor, k_scale: torch.Tenso
     """Paged MLA decode over an FP8 latent cache: k8 [pages, 64, h_kv, 576] uint8 E4M3 codes
     (or float8_e4m3fn), k_scale [h_kv, pages, 64] fp32, one scale per token and latent head;
     up to 16 query rows per latent head.  Other arguments and results as mla_decode_paged."""
+    return _decode_fp8("mla_decode_paged_fp8", q, k8, k_scale, block_table, cache_seqlens, dv, tile_metadata,
+                       num_splits, softmax_scale, causal, workspace, out, lse, skip_combine)
+
+
+def mla_decode_paged_fp8_rows(q: torch.Tensor, k8: torch.Tensor, k_scale: torch.Tensor, block_table: torch.Tensor,
+                              cache_seqlens: torch.Tensor, dv: int, tile_metadata: torch.Tensor,
+                              num_splits: torch.Tensor, softmax_scale: Optional[float] = None,
+                              causal: bool = False, workspace: Optional[torch.Tensor] = None,
+                              out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                              skip_combine: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """mla_decode_paged_fp8 for any number of query rows per latent head (above 16 a CTA-pair
+    tensor-core kernel on the codes themselves)."""
+    return _decode_fp8("mla_decode_paged_fp8_rows", q, k8, k_scale, block_table, cache_seqlens, dv, tile_metadata,
+                       num_splits, softmax_scale, causal, workspace, out, lse, skip_combine)
+
+
+def _decode_fp8(entry, q, k8, k_scale, block_table, cache_seqlens, dv, tile_metadata, num_splits, softmax_scale, causal,
+                workspace, out, lse, skip_combine) -> Tuple[torch.Tensor, torch.Tensor]:
     _require_cuda(q, "q", torch.bfloat16)
     if k8.dtype == torch.float8_e4m3fn:
         k8 = k8.view(torch.uint8)
@@ -383,7 +403,7 @@ def mla_decode_paged_fp8(q: torch.Tensor, k8: torch.Tensor, k_scale: torch.Tenso
     if workspace is None:
         workspace = _default_workspace(workspace_size(b, s_q, h_q, h_kv, num_parts), dev)
     qst = q.stride()
-    _check(load_library().mla_decode_paged_fp8(
+    _check(getattr(load_library(), entry)(
         q.data_ptr(), _I64x3(qst[0], qst[1], qst[2]), b, s_q, h_q, d, k8.data_ptr(), k_scale.data_ptr(),
         num_pages, page, h_kv, block_table.data_ptr(), block_table.stride(0), cache_seqlens.data_ptr(), dv,
         tile_metadata.data_ptr(), num_parts, num_splits.data_ptr(), scale, int(bool(causal)), out.data_ptr(),
