@@ -38,9 +38,12 @@
 // Warp roles (both CTAs):
 //   warp 0      producer: own pages and the group's key scales, the partner page's value half
 //   warp 1      tensor-memory owner; in CTA 0 the MMA issuer (one thread)
-//   warps 2-5   softmax, O rescale and epilogue: lane l of sub-partition q owns row (32 q + l) mod 64
-//               and half q / 2 (keys of that page; value columns 256 (q / 2) + 0..255)
-//   warps 6-9   query loaders: 16 rows each, split into q_hi and q_lo
+//   warps 2-9   softmax, O rescale and epilogue: lane l of sub-partition q owns row (32 q + l) mod 64
+//               and half q / 2 (keys of that page; value columns 256 (q / 2) + 0..255), of which the
+//               two warps of a sub-partition take 32 keys and 128 columns each.  Splitting P is the
+//               longest stage: one warp per sub-partition took 3.0 us a group, against 1.6 us of MMAs
+//   warps 10-15 query loaders: 11 rows each (9 the last), split into q_hi and q_lo and held in registers
+//               until the previous query tile is free
 // Every wait is bounded.
 #include <cuda_fp8.h>
 
@@ -51,17 +54,18 @@ namespace pagedmla {
 namespace {
 
 struct FpPair {
-  static constexpr int kThreads = 320;
+  static constexpr int kThreads = 512;
   static constexpr int BM = 64;                  // query rows per CTA
   static constexpr int kStages = 3;
   static constexpr int kBlock = 64 * 128;        // bytes of a block
   static constexpr int kPageBlocks = 5;          // column blocks of a page (the last one half filled)
   static constexpr int kSlots = kPageBlocks + 1;
+  static constexpr int kLoaders = 6, kLoadRows = 11;  // warps, and query rows of a warp
   static constexpr int kQScales = 8;             // row-scale buffers, by piece
   static constexpr int kOffRing = 0;
   static constexpr int kOffQ = kOffRing + kStages * kSlots * kBlock;
-  static constexpr int kOffX = kOffQ + 9 * kBlock;            // row-max exchange [2][2][64], row sums [2][64]
-  static constexpr int kOffSc = kOffX + (4 + 2) * 64 * 4;     // key scales [stage][128]
+  static constexpr int kOffX = kOffQ + 9 * kBlock;            // row-max exchange [2][4][64], row sums [4][64]
+  static constexpr int kOffSc = kOffX + (8 + 4) * 64 * 4;     // key scales [stage][128]
   static constexpr int kOffQSc = kOffSc + kStages * 128 * 4;  // row scales [8][64]
   enum {
     FULL = 0, VFULL = FULL + kStages, EMPTY = VFULL + kStages, SFULL = EMPTY + kStages, SFREE = SFULL + kStages,
@@ -116,26 +120,40 @@ __device__ __forceinline__ void load_for_pair(uint32_t dst, const CUtensorMap *m
       : "memory");
 }
 
+// The same of two neighbouring column blocks of a page at once (blocks_map: columns of a block,
+// tokens, blocks, latent heads): pair 0 is value columns 0-255, pair 1 256-511.
+__device__ __forceinline__ void load_blocks_for_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar_cluster,
+                                                     int token, int head, int block_pair, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(0), "r"(token), "r"(2 * block_pair), "r"(head),
+      "l"(policy)
+      : "memory");
+}
+
 // Instruction descriptor of kind::f8f6f4 with fp32 D and E4M3 B; A is E4M3, or E5M2 (a_e5m2).
 __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_e5m2, bool b_mn_major) {
   return (1u << 4) | (uint32_t(a_e5m2) << 7) | (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) |
          (uint32_t(M >> 4) << 24);
 }
 
+// The issuing warp runs converged and one elected lane (the same each time) issues: descriptors
+// that are uniform over the warp stay in uniform registers.
 __device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 
 // Arrive once on the barrier at this offset in both CTAs when all tcgen05 work issued so far by
-// this thread is done.
+// the elected lane is done.
 __device__ __forceinline__ void commit_both(uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar)
+      "{\n\t.reg .b16 m;\n\t.reg .pred e;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar)
       : "memory");
 }
 
@@ -151,18 +169,77 @@ __device__ __forceinline__ void tmem_store32(uint32_t taddr, const float (&v)[32
       : "memory");
 }
 
+// Element k of lane l of each group of N neighbouring lanes becomes element l of lane k.
+template <int N>
+__device__ __forceinline__ void transpose_lanes(uint4 (&u)[N], int lane) {
+#pragma unroll
+  for (int d = 1; d < N; d <<= 1) {
+    const bool upper = (lane & d) != 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(i & d)) {
+        uint4 &a = u[i], &b = u[i | d];
+        const uint4 send = upper ? a : b;
+        uint4 got;
+        got.x = __shfl_xor_sync(0xffffffffu, send.x, d);
+        got.y = __shfl_xor_sync(0xffffffffu, send.y, d);
+        got.z = __shfl_xor_sync(0xffffffffu, send.z, d);
+        got.w = __shfl_xor_sync(0xffffffffu, send.w, d);
+        if (upper)
+          a = got;
+        else
+          b = got;
+      }
+  }
+}
+
 __device__ __forceinline__ bool all_lanes(bool v) { return __all_sync(0xffffffffu, v); }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
 
-// Two values as 8-bit codes (low byte first), and the rest of E4M3 codes' values.
-__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+// Two values as 8-bit codes (low byte first), and the values of two E4M3 codes.
+__device__ __forceinline__ uint32_t to_e4m3x2(__half2 v) {
+  return __nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ uint32_t to_e5m2x2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
+__device__ __forceinline__ uint32_t to_e5m2x2(__half2 v) {
+  return __nv_cvt_halfraw2_to_fp8x2(__half2_raw(v), __NV_SATFINITE, __NV_E5M2);
 }
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
-  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(codes), __NV_E4M3)));
+__device__ __forceinline__ __half2 from_e4m3x2(uint32_t codes) {
+  return __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(codes), __NV_E4M3));
+}
+
+// Largest magnitude of eight bf16 values, as its bits (non-negative values order as integers).
+__device__ __forceinline__ uint32_t bf16_top(const uint4 &u) {
+  const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m = max(m, max(w4[k] & 0x7fffu, (w4[k] >> 16) & 0x7fffu));
+  return m;
+}
+
+// A query row's power of two, 2^(7 - (e - 127)) for the biased exponent e of its largest value; a
+// row with an infinity or NaN becomes NaN.
+__device__ __forceinline__ float row_up(int e) { return e == 255 ? __int_as_float(0x7fffffff) : pow2(134 - e); }
+
+// Eight bf16 values times `up` as E4M3 codes (x, y), and the codes of the rest (z, w).  Between
+// 2^-16 and 256 the scaled values are f16 values (smaller ones are off by at most 2^-25).
+__device__ __forceinline__ uint4 split_q(const uint4 &u, float up) {
+  const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+  uint32_t h[4], lw[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __half2 x = __floats2half2_rn(__uint_as_float(w4[k] << 16) * up, __uint_as_float(w4[k] & 0xffff0000u) * up);
+    h[k] = to_e4m3x2(x);
+    lw[k] = to_e4m3x2(__hsub2(x, from_e4m3x2(h[k])));
+  }
+  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, lw[0] | lw[1] << 16, lw[2] | lw[3] << 16);
+}
+
+// Four values as E4M3 codes, and the rests in E5M2 (through f16: 2^-11 of the value).
+__device__ __forceinline__ void split_v(const float (&v)[4], uint32_t &hi, uint32_t &lo) {
+  const __half2 x0 = __floats2half2_rn(v[0], v[1]), x1 = __floats2half2_rn(v[2], v[3]);
+  const uint32_t h0 = to_e4m3x2(x0), h1 = to_e4m3x2(x1);
+  hi = h0 | h1 << 16;
+  lo = to_e5m2x2(__hsub2(x0, from_e4m3x2(h0))) | to_e5m2x2(__hsub2(x1, from_e4m3x2(h1))) << 16;
 }
 
 // ------------------------------------------------------------------------------------
@@ -232,8 +309,8 @@ struct Groups {
 // The pair is the cluster's x dimension (grid x = the CTAs of the 128-row blocks, y = parts, z =
 // latent heads).
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
-    decode_fp8_pair_kernel(const __grid_constant__ CUtensorMap k8_map, const DecodeParams p,
-                           const float *__restrict__ k_scale, int64_t scale_head) {
+    decode_fp8_pair_kernel(const __grid_constant__ CUtensorMap k8_map, const __grid_constant__ CUtensorMap blocks_map,
+                           const DecodeParams p, const float *__restrict__ k_scale, int64_t scale_head) {
   using T = FpPair;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -249,8 +326,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
   volatile int *abort = reinterpret_cast<volatile int *>(smem + T::kOffAbort);
   const uint32_t sQ = sbase + T::kOffQ;
   auto slot = [&](int st, int k) { return sbase + uint32_t(T::kOffRing + (st * T::kSlots + k) * T::kBlock); };
-  float *xmax = reinterpret_cast<float *>(smem + T::kOffX);  // [2 parity][2 half][64 rows]
-  float *xsum = xmax + 4 * 64;                                // [2 half][64 rows]
+  float *xmax = reinterpret_cast<float *>(smem + T::kOffX);  // [2 parity][4 key quarters][64 rows]
+  float *xsum = xmax + 8 * 64;                                // [4 key quarters][64 rows]
   float *qscale = reinterpret_cast<float *>(smem + T::kOffQSc);
   const bool leader = rank == 0;
 
@@ -260,14 +337,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
       mbar_init(bar(T::VFULL + i), 1);
       mbar_init(bar(T::EMPTY + i), 1);
       mbar_init(bar(T::SFULL + i), 1);
-      mbar_init(bar(T::SFREE + i), 8);
-      mbar_init(bar(T::PFULL + i), 8);
+      mbar_init(bar(T::SFREE + i), 16);
+      mbar_init(bar(T::PFULL + i), 16);
       mbar_init(bar(T::SCALES + i), 1);
     }
-    for (int i = 0; i < T::kQScales; ++i) mbar_init(bar(T::QSC + i), 4);
+    for (int i = 0; i < T::kQScales; ++i) mbar_init(bar(T::QSC + i), T::kLoaders);
     mbar_init(bar(T::OFULL), 1);
-    mbar_init(bar(T::OFREE), 8);
-    mbar_init(bar(T::QFULL), 8);
+    mbar_init(bar(T::OFREE), 16);
+    mbar_init(bar(T::QFULL), 2 * T::kLoaders);
     mbar_init(bar(T::QFREE), 1);
     mbar_init(bar(T::FINAL), 1);
     *abort = 0;
@@ -289,77 +366,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
   const unsigned long long lim_ns = p.watchdog_ns;
 
   if (warp == 0) {
-    // ------------------------- producer (one thread in both CTAs) -------------------------
+    // ------------------------- producer (one warp in both CTAs) -------------------------
+    // The warp runs converged; one instruction issues a step's copies from several lanes.
     if (lane == 0) {
       prefetch_tensormap(&k8_map);
-      // pages are read by both CTAs of the pair (the second time from L2)
-      const uint64_t policy = l2_evict_normal_policy();
-      const float *scales = k_scale + int64_t(kvh) * scale_head;
-      const bool prefetch = p.h_kv == 1;
-      Groups wa, wb, wf;  // own pages, partner value halves, L2 prefetch ahead of the own pages
-      wa.start(p, pc, prow0);
-      wb = wa;
-      wf = wa;
-      if (prefetch)
-        for (int i = 0; i < T::kStages && !wf.done; ++i) wf.next(p, pc, prow0);
-      bool ok = true;
-      unsigned long long idle_since = 0;
-      uint32_t spins = 0;
-      while (ok && (!wa.done || wb.count < wa.count)) {
-        bool progressed = false;
-        // the partner page's value half of a group, once its score is done
-        if (wb.count < wa.count && mbar_test_wait(bar(T::SFULL + wb.stage), wb.phase)) {
-          int pa, pb;
-          wb.pages(p, pa, pb);
-          const int phys = leader ? pb : pa;
+      prefetch_tensormap(&blocks_map);
+    }
+    // pages are read by both CTAs of the pair (the second time from L2)
+    const uint64_t policy = l2_evict_normal_policy();
+    const float *scales = k_scale + int64_t(kvh) * scale_head;
+    const bool prefetch = p.h_kv == 1;
+    Groups wa, wb, wf;  // own pages, partner value halves, L2 prefetch ahead of the own pages
+    wa.start(p, pc, prow0);
+    wb = wa;
+    wf = wa;
+    if (prefetch)  // the first loads go to the ring and the query alone
+      for (int i = 0; i < 2 * T::kStages && !wf.done; ++i) wf.next(p, pc, prow0);
+    bool ok = true;
+    unsigned long long idle_since = 0;
+    uint32_t spins = 0;
+    while (ok && (!wa.done || wb.count < wa.count)) {
+      bool progressed = false;
+      // the partner page's value half of a group, once its score is done
+      if (wb.count < wa.count && all_lanes(mbar_test_wait(bar(T::SFULL + wb.stage), wb.phase))) {
+        int pa, pb;
+        wb.pages(p, pa, pb);
+        if (lane == 0) {
           if (leader) mbar_arrive_expect_tx(bar(T::VFULL + wb.stage), 2 * T::kHalfVBytes);
-          for (int c = 0; c < 2; ++c)
-            load_for_pair(slot(wb.stage, leader ? 2 + c : c), &k8_map, bar_cta0(T::VFULL + wb.stage),
-                          (leader ? c : 2 + c) * 128, kvh, phys * kPage, policy);
-          wb.next(p, pc, prow0);
-          progressed = true;
+          load_blocks_for_pair(slot(wb.stage, leader ? 2 : 0), &blocks_map, bar_cta0(T::VFULL + wb.stage),
+                               (leader ? pb : pa) * kPage, kvh, leader ? 0 : 1, policy);
         }
-        // the own page and the scales of a group, once the products of the stage's last group are done
-        if (!progressed && !wa.done &&
-            (wa.count < T::kStages || mbar_test_wait(bar(T::EMPTY + wa.stage), wa.phase ^ 1))) {
-          int pa, pb;
-          wa.pages(p, pa, pb);
-          const int phys = leader ? pa : pb, st = wa.stage;
-          if (leader) mbar_arrive_expect_tx(bar(T::FULL + st), 2 * T::kOwnBytes);
-          const uint32_t fb = bar_cta0(T::FULL + st);
-#pragma unroll
-          for (int c = 0; c < T::kPageBlocks; ++c) load_for_pair(slot(st, c), &k8_map, fb, c * 128, kvh, phys * kPage, policy);
-          const uint32_t sc = sbase + T::kOffSc + st * 512;
-          mbar_arrive_expect_tx(bar(T::SCALES + st), 512);
-          bulk_load_hint(sc, scales + int64_t(pa) * kPage, 256, bar(T::SCALES + st), policy);
-          bulk_load_hint(sc + 256, scales + int64_t(pb) * kPage, 256, bar(T::SCALES + st), policy);
-          if (prefetch && !wf.done) {
-            int fa, fb2;
-            wf.pages(p, fa, fb2);
-            prefetch_l2_bulk(p.kv_base + int64_t(leader ? fa : fb2) * kPage * p.kv_token_bytes, kPage * kD);
-            wf.next(p, pc, prow0);
-          }
-          wa.next(p, pc, prow0);
-          progressed = true;
-        }
-        if (progressed) {
-          idle_since = 0;
-        } else if (__nanosleep(32), (++spins & 15u) == 0) {
-          const unsigned long long now = global_ns();
-          if (*abort) {
-            ok = false;
-          } else if (idle_since == 0) {
-            idle_since = now;
-          } else if (now - idle_since > lim_ns) {
-            *abort = 1;
-            report_timeout(p.status);
-            ok = false;
-          }
-        }
+        __syncwarp();
+        wb.next(p, pc, prow0);
+        progressed = true;
       }
-      // Every copy issued lands before the CTAs exit: the scales on this CTA's barriers, the pages
-      // of both CTAs on CTA 0's (CTA 1 leaves after CTA 0: the final cluster barrier).  The last
-      // group of each stage is the one to wait for.
+      // the own page and the scales of a group, once the products of the stage's last group are done
+      if (!progressed && !wa.done &&
+          (wa.count < T::kStages || all_lanes(mbar_test_wait(bar(T::EMPTY + wa.stage), wa.phase ^ 1)))) {
+        int pa, pb;
+        wa.pages(p, pa, pb);
+        const int phys = leader ? pa : pb, st = wa.stage;
+        if (lane == 0) {
+          if (leader) mbar_arrive_expect_tx(bar(T::FULL + st), 2 * T::kOwnBytes);
+          mbar_arrive_expect_tx(bar(T::SCALES + st), 512);
+        }
+        __syncwarp();
+        if (lane < 2)
+          load_blocks_for_pair(slot(st, 2 * lane), &blocks_map, bar_cta0(T::FULL + st), phys * kPage, kvh, lane, policy);
+        else if (lane == 2)
+          load_for_pair(slot(st, 4), &k8_map, bar_cta0(T::FULL + st), 512, kvh, phys * kPage, policy);
+        else if (lane < 5)
+          bulk_load_hint(sbase + T::kOffSc + st * 512 + (lane - 3) * 256, scales + int64_t(lane == 3 ? pa : pb) * kPage, 256,
+                         bar(T::SCALES + st), policy);
+        __syncwarp();
+        if (prefetch && wa.count >= T::kStages && !wf.done) {
+          int fa, fb;
+          wf.pages(p, fa, fb);
+          if (lane == 0)
+            prefetch_l2_bulk(p.kv_base + int64_t(leader ? fa : fb) * kPage * p.kv_token_bytes, kPage * kD);
+          __syncwarp();
+          wf.next(p, pc, prow0);
+        }
+        wa.next(p, pc, prow0);
+        progressed = true;
+      }
+      if (progressed) {
+        idle_since = 0;
+      } else if (__nanosleep(32), (++spins & 15u) == 0) {
+        const unsigned long long now = global_ns();
+        if (*abort) {
+          ok = false;
+        } else if (idle_since == 0) {
+          idle_since = now;
+        } else if (now - idle_since > lim_ns) {
+          *abort = 1;
+          if (lane == 0) report_timeout(p.status);
+          ok = false;
+        }
+        ok = all_lanes(ok);
+      }
+    }
+    // Every copy issued lands before the CTAs exit: the scales on this CTA's barriers, the pages
+    // of both CTAs on CTA 0's (CTA 1 leaves after CTA 0: the final cluster barrier).  The last
+    // group of each stage is the one to wait for.
+    if (lane == 0) {
       int never = 0;
       for (int i = 1; i <= T::kStages; ++i) {
         const int ga = wa.count - i, gb = wb.count - i;
@@ -372,83 +462,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (leader && lane == 0) {
-      // ------------------------- MMA issuer (CTA 0, one thread) -------------------------
+    if (leader) {
+      // ------------------------- MMA issuer (CTA 0, one warp) -------------------------
       // The score of a group needs its pages in both CTAs (FULL), the query tile (QFULL) and its
       // score buffer read (SFREE); its PV needs both CTAs' v tiles (PFULL) and partner halves
-      // (VFULL), and at a piece's first group the previous epilogue (OFREE).  Scores run at most
-      // kStages groups ahead of PV, and PV goes first when both are ready.
+      // (VFULL), and at a piece's first group the previous epilogue (OFREE).  Scores run up to
+      // kStages groups ahead of PV; when both are ready the score goes first until it is two groups
+      // ahead.  A poll of shared memory takes some 200 cycles beside the MMAs' operand reads, so the
+      // barriers of a step are polled together, and none of them again once it has been seen.
       const uint32_t idesc_qk = idesc_f8(128, 128, false, false);
       const uint32_t idesc_hi = idesc_f8(128, 256, false, true), idesc_lo = idesc_f8(128, 256, true, true);
       Groups wq, wv;
       wq.start(p, pc, prow0);
       wv = wq;
       int qpiece = 0, vpiece = 0;
-      bool have_q = false, ok = true;
+      bool qk_ready = false, pv_ready = false, ok = true;
       unsigned long long idle_since = 0;
       uint32_t spins = 0;
       while (ok && !wv.done) {
-        bool progressed = false;
-        if (wv.count < wq.count) {
+        bool q1 = true, q2 = true, q3 = true, v1 = true, v2 = true, v3 = true;
+        const bool poll_qk = !qk_ready && !wq.done && wq.count < wv.count + T::kStages;
+        const bool poll_pv = !pv_ready && wv.count < wq.count;
+        if (poll_qk) {
+          q1 = mbar_test_wait(bar(T::FULL + wq.stage), wq.phase);
+          if (wq.count >= T::kStages) q2 = mbar_test_wait(bar(T::SFREE + wq.stage), wq.phase ^ 1);
+          if (wq.j == 0) q3 = mbar_test_wait(bar(T::QFULL), qpiece & 1);
+        }
+        if (poll_pv) {
+          v1 = mbar_test_wait(bar(T::PFULL + wv.stage), wv.phase);
+          v2 = mbar_test_wait(bar(T::VFULL + wv.stage), wv.phase);
+          if (wv.j == 0 && vpiece > 0) v3 = mbar_test_wait(bar(T::OFREE), (vpiece - 1) & 1);
+        }
+        if (poll_qk) qk_ready = all_lanes(q1 && q2 && q3);
+        if (poll_pv) pv_ready = all_lanes(v1 && v2 && v3);
+        if (qk_ready && (!pv_ready || wq.count < wv.count + 2)) {
+          tc_fence_after();
+          const int st = wq.stage;
+          const uint32_t d = tmem + T::kTmemS + 64 * st;
+          const uint64_t kb = smem_desc_sw128(slot(st, 0), 16, 1024), qa = smem_desc_sw128(sQ, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kD / 32; ++kk) {
+            const int cb = kk >> 2, in = (kk & 3) * 32;
+            // descriptors step by (byte offset >> 4) in their address field
+            const uint64_t b = kb + uint64_t((cb * T::kBlock + in) >> 4);
+            const uint64_t hi = uint64_t((cb < 4 ? cb * T::kBlock + in : 8 * T::kBlock + in) >> 4);
+            const uint64_t lo = uint64_t((cb < 4 ? (4 + cb) * T::kBlock + in : 8 * T::kBlock + 64 + in) >> 4);
+            mma_f8_pair(d, qa + hi, b, idesc_qk, kk > 0 ? 1u : 0u);
+            mma_f8_pair(d, qa + lo, b, idesc_qk, 1u);
+          }
+          commit_both(bar(T::SFULL + st));
+          if (wq.j + 1 == wq.ngroups) {
+            commit_both(bar(T::QFREE));  // the query tile may be replaced
+            ++qpiece;
+          }
+          wq.next(p, pc, prow0);
+          qk_ready = false;
+          idle_since = 0;
+        } else if (pv_ready) {
+          tc_fence_after();
           const int st = wv.stage;
           const bool first = wv.j == 0;
-          if (mbar_test_wait(bar(T::PFULL + st), wv.phase) && mbar_test_wait(bar(T::VFULL + st), wv.phase) &&
-              (!first || vpiece == 0 || mbar_test_wait(bar(T::OFREE), (vpiece - 1) & 1))) {
-            tc_fence_after();
-            // a lone last page: the second page's keys are masked (v = 0), skip their products
-            const int halves = (2 * wv.j + 1 < wv.ntiles) ? 2 : 1;
-            // descriptors step by (byte offset >> 4) in their address field
-            const uint64_t hi = smem_desc_sw128(slot(st, 4), 16, 1024), lo = smem_desc_sw128(slot(st, 5), 16, 1024);
-            const uint64_t vb = smem_desc_sw128(slot(st, 0), T::kBlock, 1024);
-            for (int h = 0; h < halves; ++h)
+          // a lone last page: the second page's keys are masked (v = 0), skip their products
+          const int halves = (2 * wv.j + 1 < wv.ntiles) ? 2 : 1;
+          const uint64_t hi = smem_desc_sw128(slot(st, 4), 16, 1024), lo = smem_desc_sw128(slot(st, 5), 16, 1024);
+          const uint64_t vb = smem_desc_sw128(slot(st, 0), T::kBlock, 1024);
+          for (int h = 0; h < halves; ++h)
 #pragma unroll
-              for (int ks = 0; ks < 2; ++ks)
+            for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                  const uint64_t a = uint64_t((h * 64 + ks * 32) >> 4);
-                  const uint64_t b = vb + uint64_t(((2 * h + v) * T::kBlock + ks * 4096) >> 4);
-                  mma_f8_pair(tmem + T::kTmemO + 128 * v, hi + a, b, idesc_hi, (!first || h > 0 || ks > 0) ? 1u : 0u);
-                  mma_f8_pair(tmem + T::kTmemO + 128 * v, lo + a, b, idesc_lo, 1u);
-                }
-            commit_both(bar(T::EMPTY + st));
-            if (wv.j + 1 == wv.ngroups) {
-              commit_both(bar(T::OFULL));
-              ++vpiece;
-            }
-            wv.next(p, pc, prow0);
-            progressed = true;
+              for (int v = 0; v < 2; ++v) {
+                const uint64_t a = uint64_t((h * 64 + ks * 32) >> 4);
+                const uint64_t b = vb + uint64_t(((2 * h + v) * T::kBlock + ks * 4096) >> 4);
+                mma_f8_pair(tmem + T::kTmemO + 128 * v, hi + a, b, idesc_hi, (!first || h > 0 || ks > 0) ? 1u : 0u);
+                mma_f8_pair(tmem + T::kTmemO + 128 * v, lo + a, b, idesc_lo, 1u);
+              }
+          commit_both(bar(T::EMPTY + st));
+          if (wv.j + 1 == wv.ngroups) {
+            commit_both(bar(T::OFULL));
+            ++vpiece;
           }
-        }
-        if (!progressed && !wq.done && wq.count < wv.count + T::kStages) {
-          const int st = wq.stage;
-          if (!have_q) have_q = mbar_test_wait(bar(T::QFULL), qpiece & 1);
-          if (have_q && mbar_test_wait(bar(T::FULL + st), wq.phase) &&
-              (wq.count < T::kStages || mbar_test_wait(bar(T::SFREE + st), wq.phase ^ 1))) {
-            tc_fence_after();
-            const uint32_t d = tmem + T::kTmemS + 64 * st;
-            const uint64_t kb = smem_desc_sw128(slot(st, 0), 16, 1024), qa = smem_desc_sw128(sQ, 16, 1024);
-#pragma unroll
-            for (int kk = 0; kk < kD / 32; ++kk) {
-              const int cb = kk >> 2, in = (kk & 3) * 32;
-              const uint64_t b = kb + uint64_t((cb * T::kBlock + in) >> 4);
-              const uint64_t hi = uint64_t((cb < 4 ? cb * T::kBlock + in : 8 * T::kBlock + in) >> 4);
-              const uint64_t lo = uint64_t((cb < 4 ? (4 + cb) * T::kBlock + in : 8 * T::kBlock + 64 + in) >> 4);
-              mma_f8_pair(d, qa + hi, b, idesc_qk, kk > 0 ? 1u : 0u);
-              mma_f8_pair(d, qa + lo, b, idesc_qk, 1u);
-            }
-            commit_both(bar(T::SFULL + st));
-            if (wq.j + 1 == wq.ngroups) {
-              commit_both(bar(T::QFREE));  // the query tile may be replaced
-              have_q = false;
-              ++qpiece;
-            }
-            wq.next(p, pc, prow0);
-            progressed = true;
-          }
-        }
-        if (progressed) {
+          wv.next(p, pc, prow0);
+          pv_ready = false;
           idle_since = 0;
-        } else if (__nanosleep(32), (++spins & 15u) == 0) {
+        } else if ((++spins & 15u) == 0) {
           const unsigned long long now = global_ns();
           if (*abort) {
             ok = false;
@@ -456,9 +552,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
             idle_since = now;
           } else if (now - idle_since > lim_ns) {
             *abort = 1;
-            report_timeout(p.status);
+            if (lane == 0) report_timeout(p.status);
             ok = false;
           }
+          ok = all_lanes(ok);
         }
       }
       commit_both(bar(T::FINAL));
@@ -471,16 +568,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
       mbar_wait(bar(T::FINAL), 0, &never, p.status, lim_ns);
     }
     __syncwarp();
-  } else if (warp < 6) {
+  } else if (warp < 10) {
     // ------------------------- softmax / O rescale / epilogue -------------------------
     const int q = warp & 3;                 // tensor-memory sub-partition of this warp
     const int lrow = (32 * q + lane) & 63;  // row within the CTA's 64
     const int hf = q >> 1;                  // 0: first page's keys, values 0-255; 1: second page, 256-511
+    const int quarter = 2 * hf + (warp - 2) / 4;  // this warp's 32 of the group's keys
+    const int col0 = 128 * ((warp - 2) / 4);      // and its 128 of the half's 256 columns
     const int row = crow0 + lrow;
     const bool active = row < p.R;
     const int s_row = row / p.g, h_row = kvh * p.g + row % p.g;
     const uint32_t lanes = tmem + (uint32_t(32 * q) << 16);
-    const int xbar = 1 + (q & 1);           // named barrier of the two warps sharing rows
+    const int xbar = 1 + (q & 1);           // named barrier of the four warps sharing rows
     const uint32_t sfree = bar_cta0(T::SFREE), pfull = bar_cta0(T::PFULL), ofree = bar_cta0(T::OFREE);
     int g = 0, st = 0, phase = 0, last_st = 0, last_phase = 0, qs = 0;
     bool ok = true;
@@ -490,18 +589,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
       const int nsplit = split_base(p.num_splits, seq + 1) - ns0;
       const int ord = seq == pc.bi ? pc.bord : 0;
       const int64_t acc_row = (int64_t(ns0 + ord) * p.h_kv + kvh) * p.R + row;
-      __nv_bfloat16 *out_row = p.out + ((int64_t(seq) * p.s_q + s_row) * p.h_q + h_row) * kDV + hf * 256;
+      __nv_bfloat16 *out_row = p.out + ((int64_t(seq) * p.s_q + s_row) * p.h_q + h_row) * kDV + hf * 256 + col0;
+      float *acc_out = p.o_accum + acc_row * kDV + hf * 256 + col0;
       float *lse_row = p.lse + (int64_t(seq) * p.h_q + h_row) * p.s_q + s_row;
       if (w.ngroups == 0) {
         // no visible key in this piece: zero output (or partial) and lse = -inf
         if (active) {
           if (nsplit == 1) {
-            for (int i = 0; i < 32; ++i) reinterpret_cast<uint4 *>(out_row)[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (hf == 0) *lse_row = -INFINITY;
+            for (int i = 0; i < 16; ++i) reinterpret_cast<uint4 *>(out_row)[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (quarter == 0) *lse_row = -INFINITY;
           } else {
-            float4 *o = reinterpret_cast<float4 *>(p.o_accum + acc_row * kDV + hf * 256);
-            for (int i = 0; i < 64; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (hf == 0) p.lse_accum[acc_row] = -INFINITY;
+            for (int i = 0; i < 32; ++i) reinterpret_cast<float4 *>(acc_out)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (quarter == 0) p.lse_accum[acc_row] = -INFINITY;
           }
         }
         continue;
@@ -512,27 +611,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
       // score of raw products to log2 units: 2^-a of the row and the softmax scale
       // (kept above 0, so that a masked score stays -inf)
       const float rowf = fmaxf(qscale[(qs & (T::kQScales - 1)) * 64 + lrow] * p.scale_log2, 1.2e-38f);
-      float m_used = -INFINITY, l = 0.f;  // l: this thread's half of the row sum
+      float m_used = -INFINITY, l = 0.f;  // l: this thread's quarter of the row sum
       int e_used = -100;                  // every key scale of the piece so far is below 2^e_used
       for (int j = 0; j < w.ngroups; ++j, ++g) {
-        ok = all_lanes(ok && mbar_wait(bar(T::SFULL + st), phase, abort, p.status, lim_ns));
         ok = all_lanes(ok && mbar_wait(bar(T::SCALES + st), phase, abort, p.status, lim_ns));
-        tc_fence_after();
-        float sv[64];
-        if (ok) {
-          float t[32];
-          tmem_ld32(lanes + T::kTmemS + 64 * st, t);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) sv[i] = t[i];
-          tmem_ld32(lanes + T::kTmemS + 64 * st + 32, t);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) sv[32 + i] = t[i];
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(sfree + 8u * st);
         const float4 *sc4 = reinterpret_cast<const float4 *>(smem + T::kOffSc + st * 512);
-        const int group0 = w.t0 + 128 * j, key0 = group0 + 64 * hf;
+        const int group0 = w.t0 + 128 * j, key0 = group0 + 32 * quarter;
         // the largest scale of the group's keys, the same in every thread of the pair; slots past the
         // piece's end are not keys and their scales are never used
         const float4 mine = sc4[lane];
@@ -543,29 +627,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
         if (left > 2) sb = max(sb, __float_as_uint(fabsf(mine.z)));
         if (left > 3) sb = max(sb, __float_as_uint(fabsf(mine.w)));
         const int e_new = max(e_used, int(__reduce_max_sync(0xffffffffu, sb) >> 23) - 126);
-        const bool partial = key0 + 64 > lim;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float4 s = sc4[16 * hf + i];
-          sv[4 * i] *= s.x;
-          sv[4 * i + 1] *= s.y;
-          sv[4 * i + 2] *= s.z;
-          sv[4 * i + 3] *= s.w;
-        }
-        // keys at or past this row's limit get -inf (only partial groups need the test)
-        if (partial) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (key0 + i >= lim) sv[i] = -INFINITY;
-        }
+        const float f = pow2(6 - e_new);
+        ok = all_lanes(ok && mbar_wait(bar(T::SFULL + st), phase, abort, p.status, lim_ns));
+        tc_fence_after();
+        float sv[32];
+        if (ok) tmem_ld32(lanes + T::kTmemS + 64 * st + 32 * (quarter & 1), sv);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(sfree + 8u * st);
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
+        for (int i = 0; i < 8; ++i) {
+          const float4 s = sc4[8 * quarter + i];
+          const float ks[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sv[4 * i + k] *= ks[k];
+        }
+        // keys at or past this row's limit get -inf (only partial groups need the test)
+        const bool partial = __any_sync(0xffffffffu, key0 + 32 > lim);
+        if (partial) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (key0 + i >= lim) sv[i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
         float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rowf;
-        // the row's other half lives on the partner warp: exchange maxima
-        xmax[((g & 1) * 2 + hf) * 64 + lrow] = mx;
-        named_bar_sync(xbar, 64);
-        mx = fmaxf(mx, xmax[((g & 1) * 2 + (hf ^ 1)) * 64 + lrow]);
+        // the row's other keys live on the partner warps: exchange maxima
+        float *xm = xmax + (g & 1) * 4 * 64 + lrow;
+        xm[quarter * 64] = mx;
+        named_bar_sync(xbar, 128);
+        mx = fmaxf(fmaxf(xm[0], xm[64]), fmaxf(xm[128], xm[192]));
         // The running maximum is refreshed when it grows by more than 2 (log2 units), so P stays
         // below 4 and v = P s 2^(6-e) below 256, inside E4M3
         const float m_new = fmaxf(m_used, mx);
@@ -580,25 +672,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
         const bool rescale = j > 0 && (__any_sync(0xffffffffu, need) || e_new > e_used);
         alpha *= e_new - e_used < 127 ? pow2(-min(e_new - e_used, 126)) : 0.f;
         e_used = e_new;
-        const float f = pow2(6 - e_used);
-        uint32_t hi[16], lo[16];
+        uint32_t hi[8], lo[8];
         float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float4 s = sc4[16 * hf + i];
-          float v[4];
+        for (int i = 0; i < 8; ++i) {
+          const float4 s = sc4[8 * quarter + i];
           const float ks[4] = {s.x, s.y, s.z, s.w};
+          float v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float e = fast_exp2(fmaf(sv[4 * i + k], rowf, nbase));
             s4[k] += e;
             v[k] = e * (ks[k] * f);
-            if (partial && key0 + 4 * i + k >= lim) v[k] = 0.f;
           }
-          const uint32_t h0 = to_e4m3x2(v[0], v[1]), h1 = to_e4m3x2(v[2], v[3]);
-          const float2 b0 = from_e4m3x2(h0), b1 = from_e4m3x2(h1);
-          hi[i] = h0 | h1 << 16;
-          lo[i] = to_e5m2x2(v[0] - b0.x, v[1] - b0.y) | to_e5m2x2(v[2] - b1.x, v[3] - b1.y) << 16;
+          if (partial) {  // the scale of a slot that is no key may be anything
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (key0 + 4 * i + k >= lim) v[k] = 0.f;
+          }
+          split_v(v, hi[i], lo[i]);
         }
         l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
         // O may be rescaled once the previous group's PV has completed (its commit arrives on EMPTY
@@ -608,7 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
           if (ok) {
             tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 0; c0 < 256; c0 += 32) {
+            for (int c0 = col0; c0 < col0 + 128; c0 += 32) {
               float v[32];
               tmem_ld32(lanes + T::kTmemO + c0, v);
 #pragma unroll
@@ -619,13 +711,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
           }
         }
         if (ok) {
-          // the two terms of v into their tiles: 64 keys are four 16-byte chunks of a row
+          // the two terms of v into their tiles: 32 keys are two 16-byte chunks of a row
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot(st, 4) + sw128(lrow, 4 * hf + c)),
+          for (int c = 0; c < 2; ++c) {
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot(st, 4) + sw128(lrow, 2 * quarter + c)),
                          "r"(hi[4 * c]), "r"(hi[4 * c + 1]), "r"(hi[4 * c + 2]), "r"(hi[4 * c + 3])
                          : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot(st, 5) + sw128(lrow, 4 * hf + c)),
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot(st, 5) + sw128(lrow, 2 * quarter + c)),
                          "r"(lo[4 * c]), "r"(lo[4 * c + 1]), "r"(lo[4 * c + 2]), "r"(lo[4 * c + 3])
                          : "memory");
           }
@@ -643,33 +735,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
       }
 
       // ---- epilogue: O / l -> output (or fp32 split partial), natural-log LSE ----
-      xsum[hf * 64 + lrow] = l;
-      named_bar_sync(xbar, 64);
-      const float l_row = l + xsum[(hf ^ 1) * 64 + lrow];
+      xsum[quarter * 64 + lrow] = l;
+      named_bar_sync(xbar, 128);
+      const float l_row = (xsum[lrow] + xsum[64 + lrow]) + (xsum[128 + lrow] + xsum[192 + lrow]);
       ok = all_lanes(ok && mbar_wait(bar(T::OFULL), qs & 1, abort, p.status, lim_ns));
       tc_fence_after();
       if (ok) {
         const float inv = l_row > 0.f ? pow2(e_used - 6) / l_row : (l_row == 0.f ? 0.f : l_row);
-        for (int c0 = 0; c0 < 256; c0 += 32) {
+        const int64_t out_off = out_row - p.out;
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 32) {
           float v[32];
-          tmem_ld32(lanes + T::kTmemO + c0, v);
-          if (!active) continue;
+          tmem_ld32(lanes + T::kTmemO + col0 + c0, v);
+          // a lane holds 32 columns of its own row; transposed over groups of lanes, a store covers
+          // whole 64- or 128-byte stretches of a row instead of 16 bytes of 32 rows
           if (nsplit == 1) {
-            uint4 *o = reinterpret_cast<uint4 *>(out_row + c0);
+            uint4 u[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              o[k] = make_uint4(pack_bf16x2(v[8 * k] * inv, v[8 * k + 1] * inv),
+              u[k] = make_uint4(pack_bf16x2(v[8 * k] * inv, v[8 * k + 1] * inv),
                                 pack_bf16x2(v[8 * k + 2] * inv, v[8 * k + 3] * inv),
                                 pack_bf16x2(v[8 * k + 4] * inv, v[8 * k + 5] * inv),
                                 pack_bf16x2(v[8 * k + 6] * inv, v[8 * k + 7] * inv));
+            transpose_lanes(u, lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int from = (lane & ~3) + k;  // the lane whose row u[k] is of
+              const int64_t off = __shfl_sync(0xffffffffu, out_off, from);
+              if (row - lane + from < p.R) *reinterpret_cast<uint4 *>(p.out + off + c0 + 8 * (lane & 3)) = u[k];
+            }
           } else {
-            float4 *o = reinterpret_cast<float4 *>(p.o_accum + acc_row * kDV + hf * 256 + c0);
+            uint4 u[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              o[k] = make_float4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
+              u[k] = make_uint4(__float_as_uint(v[4 * k] * inv), __float_as_uint(v[4 * k + 1] * inv),
+                                __float_as_uint(v[4 * k + 2] * inv), __float_as_uint(v[4 * k + 3] * inv));
+            transpose_lanes(u, lane);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int from = (lane & ~7) + k;
+              if (row - lane + from < p.R)
+                *reinterpret_cast<uint4 *>(acc_out + int64_t(from - lane) * kDV + c0 + 4 * (lane & 7)) = u[k];
+            }
           }
         }
-        if (active && hf == 0) {
+        if (active && quarter == 0) {
           const float lse_v = l_row == 0.f ? -INFINITY : (m_used + fast_log2(l_row)) * 0.69314718055994531f;
           if (nsplit == 1)
             *lse_row = lse_v;
@@ -679,110 +789,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
         }
       }
       tc_fence_before();
-      // the row-sum slots are rewritten by the next piece only after both warps have read them
-      named_bar_sync(xbar, 64);
+      // the row-sum slots are rewritten by the next piece only after all four warps have read them
+      named_bar_sync(xbar, 128);
       if (lane == 0) arrive_cluster(ofree);
       ++qs;
     }
   } else {
     // ------------------------- query loaders -------------------------
-    // A warp takes 16 rows: lane l holds 16-byte chunks l and l + 32 (8 columns each) of every row,
-    // and of the rope columns (chunks 64-71) those of rows l / 8 + 4 i.  Read and split into codes
-    // before the previous piece's query tile is free, then stored.
-    const int wq = warp - 6, row0 = wq * 16;
-    const int my_row = crow0 + row0 + (lane & 15);
-    const bool my_active = my_row < p.R;
+    // Lane l holds 16-byte chunks l and l + 32 (8 columns each) of every row of the warp, and of the
+    // rope columns (chunk 64 + l mod 8) those of rows l / 8 + 4 i.
+    constexpr int N = T::kLoadRows, NR = (N + 3) / 4;
+    static_assert(T::kLoaders * N >= T::BM && N <= 16, "every row has a loader, a row scale per half warp");
+    const int row0 = (warp - 10) * N;
+    // the row whose offset and scale this lane keeps; rows past R stand for the last one (masked later)
+    const int my_x = row0 + (lane & 15), my_row = min(crow0 + my_x, p.R - 1);
+    const bool mine = (lane & 15) < N && my_x < T::BM;
     const int64_t my_off = int64_t(my_row / p.g) * p.q_ss + int64_t(kvh * p.g + my_row % p.g) * p.q_sh;
     const uint32_t qfull = bar_cta0(T::QFULL);
+    auto chunk_of = [&](const __nv_bfloat16 *base, int i, int c) {  // chunk c of row row0 + i
+      return __ldcg(reinterpret_cast<const uint4 *>(base + __shfl_sync(0xffffffffu, my_off, i)) + c);
+    };
+    auto put = [&](int block, int x, int byte, uint32_t u, uint32_t v) {
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sQ + block * T::kBlock + sw128(x, byte >> 4) + (byte & 8)),
+                   "r"(u), "r"(v)
+                   : "memory");
+    };
     int qs = 0;
     bool ok = true;
     for (int seq = pc.bi; part_has(pc, seq); ++seq) {
       if (piece_of(p, pc, seq, prow0).ngroups == 0) continue;
       const __nv_bfloat16 *base = p.q + int64_t(seq) * p.q_sb;
-      uint4 a[16][2], r[4];
+      uint4 r[NR], a[N][2];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const bool on = __shfl_sync(0xffffffffu, int(my_active), i) != 0;
-        const uint4 *src = reinterpret_cast<const uint4 *>(base + __shfl_sync(0xffffffffu, my_off, i));
-        a[i][0] = on ? __ldcg(src + lane) : make_uint4(0u, 0u, 0u, 0u);
-        a[i][1] = on ? __ldcg(src + lane + 32) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < NR; ++i) r[i] = chunk_of(base, lane / 8 + 4 * i, 64 + lane % 8);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) a[i][c] = chunk_of(base, i, lane + 32 * c);
+      int my_e = 8;  // biased exponent of this lane's row's largest value
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        uint32_t m = max(bf16_top(a[i][0]), bf16_top(a[i][1]));
+        if (lane / 8 == i % 4) m = max(m, bf16_top(r[i / 4]));
+        m = __reduce_max_sync(0xffffffffu, m);
+        if ((lane & 15) == i) my_e = max(int(m >> 7), 8);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int x = lane / 8 + 4 * i;
-        const bool on = __shfl_sync(0xffffffffu, int(my_active), x) != 0;
-        const uint4 *src = reinterpret_cast<const uint4 *>(base + __shfl_sync(0xffffffffu, my_off, x));
-        r[i] = on ? __ldcg(src + 64 + lane % 8) : make_uint4(0u, 0u, 0u, 0u);
-      }
-      // largest magnitude of eight bf16 values, as its bits (non-negative values order as integers)
-      auto top = [](const uint4 &u) {
-        const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m = max(m, max(w4[k] & 0x7fffu, (w4[k] >> 16) & 0x7fffu));
-        return m;
-      };
-      // eight bf16 values times `up` as E4M3 codes (x, y) and the codes of the rest (z, w)
-      auto split = [](const uint4 &u, float up) {
-        const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
-        uint32_t h[4], lw[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w4[k]));
-          const float x = f.x * up, y = f.y * up;
-          h[k] = to_e4m3x2(x, y);
-          const float2 b = from_e4m3x2(h[k]);
-          lw[k] = to_e4m3x2(x - b.x, y - b.y);
-        }
-        return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, lw[0] | lw[1] << 16, lw[2] | lw[3] << 16);
-      };
-      uint32_t rope_top[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t m = top(r[i]);
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        rope_top[i] = m;
-      }
-      int my_e = 0;  // biased exponent of row (lane & 15)'s largest value
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, max(top(a[i][0]), top(a[i][1])));
-        const int e = max(int(max(m, __shfl_sync(0xffffffffu, rope_top[i / 4], (i % 4) * 8)) >> 7), 8);
-        // 2^(7 - (e - 127)); a row with an infinity or NaN becomes NaN
-        const float up = e == 255 ? __int_as_float(0x7fffffff) : pow2(134 - e);
-        a[i][0] = split(a[i][0], up);
-        a[i][1] = split(a[i][1], up);
-        if ((lane & 15) == i) my_e = e;
+      for (int i = 0; i < N; ++i) {
+        const float up = row_up(__shfl_sync(0xffffffffu, my_e, i));
+        a[i][0] = split_q(a[i][0], up);
+        a[i][1] = split_q(a[i][1], up);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = __shfl_sync(0xffffffffu, my_e, lane / 8 + 4 * i);
-        r[i] = split(r[i], e == 255 ? __int_as_float(0x7fffffff) : pow2(134 - e));
-      }
+      for (int i = 0; i < NR; ++i) r[i] = split_q(r[i], row_up(__shfl_sync(0xffffffffu, my_e, lane / 8 + 4 * i)));
       if (qs > 0) ok = all_lanes(ok && mbar_wait(bar(T::QFREE), (qs - 1) & 1, abort, p.status, lim_ns));
       if (ok) {
-        auto put = [&](int block, int x, int byte, uint32_t u, uint32_t v) {
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(sQ + block * T::kBlock + sw128(x, byte >> 4) + (byte & 8)),
-                       "r"(u), "r"(v)
-                       : "memory");
-        };
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < N; ++i)
+          if (row0 + i < T::BM) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int col = 8 * (lane + 32 * c);
-            put(col / 128, row0 + i, col % 128, a[i][c].x, a[i][c].y);
-            put(4 + col / 128, row0 + i, col % 128, a[i][c].z, a[i][c].w);
+            for (int c = 0; c < 2; ++c) {
+              const int col = 8 * (lane + 32 * c);
+              put(col / 128, row0 + i, col % 128, a[i][c].x, a[i][c].y);
+              put(4 + col / 128, row0 + i, col % 128, a[i][c].z, a[i][c].w);
+            }
           }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int x = row0 + lane / 8 + 4 * i, byte = 8 * (lane % 8);
-          put(8, x, byte, r[i].x, r[i].y);
-          put(8, x, 64 + byte, r[i].z, r[i].w);
+        for (int i = 0; i < NR; ++i) {
+          const int in = lane / 8 + 4 * i, byte = 8 * (lane % 8);
+          if (in < N && row0 + in < T::BM) {
+            put(8, row0 + in, byte, r[i].x, r[i].y);
+            put(8, row0 + in, 64 + byte, r[i].z, r[i].w);
+          }
         }
-        if (lane < 16)
-          qscale[(qs & (T::kQScales - 1)) * 64 + row0 + lane] = my_e == 255 ? __int_as_float(0x7fffffff) : pow2(my_e - 134);
+        if (lane < 16 && mine)
+          qscale[(qs & (T::kQScales - 1)) * 64 + my_x] = my_e == 255 ? __int_as_float(0x7fffffff) : pow2(my_e - 134);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -803,14 +884,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
   pair_sync();
 }
 
-cudaError_t launch_decode_fp8_pair(const CUtensorMap &k8_map, const DecodeParams &p, const float *k_scale,
+cudaError_t launch_decode_fp8_pair(const CUtensorMap &k8_map, const CUtensorMap &blocks_map, const DecodeParams &p, const float *k_scale,
                                    int64_t num_pages, cudaStream_t stream) {
   using T = FpPair;
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_fp8_pair_kernel), T::kSmemBytes);
   if (e != cudaSuccess) return e;
   const unsigned pairs = unsigned((p.R + 2 * T::BM - 1) / (2 * T::BM));
   return launch_early(decode_fp8_pair_kernel, dim3(2 * pairs, p.num_parts, p.h_kv), dim3(T::kThreads), T::kSmemBytes,
-                      stream, k8_map, p, k_scale, num_pages * kPage);
+                      stream, k8_map, blocks_map, p, k_scale, num_pages * kPage);
 }
 
 }  // namespace pagedmla
