@@ -138,14 +138,14 @@ int encode_k8_map(CUtensorMap *map, const void *k8, int64_t num_pages, int h_kv)
 }
 
 // The first 512 columns of the FP8 cache as a 4-D map (columns of a 128-column block, token, block,
-// latent head); one box = 128 columns (128-byte swizzle) x 64 tokens x 2 blocks, stored block
+// latent head); one box = 128 columns (128-byte swizzle) x 64 tokens x `blocks` blocks, stored block
 // after block.
-int encode_k8_blocks_map(CUtensorMap *map, const void *k8, int64_t num_pages, int h_kv) {
+int encode_k8_blocks_map(CUtensorMap *map, const void *k8, int64_t num_pages, int h_kv, int blocks) {
   auto enc = tensor_map_encoder();
   if (!enc) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
   cuuint64_t dims[4] = {128, cuuint64_t(num_pages) * kPage, kDV / 128, cuuint64_t(h_kv)};
   cuuint64_t strides[3] = {cuuint64_t(h_kv) * kD, 128, cuuint64_t(kD)};
-  cuuint32_t box[4] = {128, 64, 2, 1};
+  cuuint32_t box[4] = {128, 64, cuuint32_t(blocks), 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(k8), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -339,10 +339,12 @@ int decode_fp8(const void *q, const int64_t *q_strides, int batch, int s_q, int 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (R > 16) {
-    CUtensorMap blocks_map;
-    rc = encode_k8_blocks_map(&blocks_map, k8, num_pages, h_kv);
+    CUtensorMap page_map, half_map;
+    rc = encode_k8_blocks_map(&page_map, k8, num_pages, h_kv, 4);
     if (rc) return rc;
-    e = launch_decode_fp8_pair(k8_map, blocks_map, p, k_scale, num_pages, st);
+    rc = encode_k8_blocks_map(&half_map, k8, num_pages, h_kv, 2);
+    if (rc) return rc;
+    e = launch_decode_fp8_pair(k8_map, page_map, half_map, p, k_scale, num_pages, st);
   } else {
     CUtensorMap scale_map, qmap;
     rc = encode_scale_map(&scale_map, k_scale, num_pages, h_kv);

@@ -36,7 +36,8 @@
 // Tensor memory (512 columns): O (value halves at 0 and 128), S at 256, 320 and 384.
 //
 // Warp roles (both CTAs):
-//   warp 0      producer: own pages and the group's key scales, the partner page's value half
+//   warp 0      producer: own pages and the group's key scales, the partner page's value half (an L2
+//               prefetch of the pages ahead measured slower: 162 against 153 us)
 //   warp 1      tensor-memory owner; in CTA 0 the MMA issuer (one thread)
 //   warps 2-9   softmax, O rescale and epilogue: lane l of sub-partition q owns row (32 q + l) mod 64
 //               and half q / 2 (keys of that page; value columns 256 (q / 2) + 0..255), of which the
@@ -120,14 +121,14 @@ __device__ __forceinline__ void load_for_pair(uint32_t dst, const CUtensorMap *m
       : "memory");
 }
 
-// The same of two neighbouring column blocks of a page at once (blocks_map: columns of a block,
-// tokens, blocks, latent heads): pair 0 is value columns 0-255, pair 1 256-511.
+// The same of a page's value columns (page_map: all four blocks; half_map: columns 256 half + 0..255;
+// both over columns of a block, tokens, blocks, latent heads), stored block after block.
 __device__ __forceinline__ void load_blocks_for_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar_cluster,
-                                                     int token, int head, int block_pair, uint64_t policy) {
+                                                     int token, int head, int half, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
       "[%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(0), "r"(token), "r"(2 * block_pair), "r"(head),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(0), "r"(token), "r"(2 * half), "r"(head),
       "l"(policy)
       : "memory");
 }
@@ -209,11 +210,8 @@ __device__ __forceinline__ __half2 from_e4m3x2(uint32_t codes) {
 
 // Largest magnitude of eight bf16 values, as its bits (non-negative values order as integers).
 __device__ __forceinline__ uint32_t bf16_top(const uint4 &u) {
-  const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) m = max(m, max(w4[k] & 0x7fffu, (w4[k] >> 16) & 0x7fffu));
-  return m;
+  const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
 }
 
 // A query row's power of two, 2^(7 - (e - 127)) for the biased exponent e of its largest value; a
@@ -309,8 +307,8 @@ struct Groups {
 // The pair is the cluster's x dimension (grid x = the CTAs of the 128-row blocks, y = parts, z =
 // latent heads).
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
-    decode_fp8_pair_kernel(const __grid_constant__ CUtensorMap k8_map, const __grid_constant__ CUtensorMap blocks_map,
-                           const DecodeParams p, const float *__restrict__ k_scale, int64_t scale_head) {
+    decode_fp8_pair_kernel(const __grid_constant__ CUtensorMap k8_map, const __grid_constant__ CUtensorMap page_map,
+                           const __grid_constant__ CUtensorMap half_map, const DecodeParams p, const float *__restrict__ k_scale, int64_t scale_head) {
   using T = FpPair;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -370,18 +368,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
     // The warp runs converged; one instruction issues a step's copies from several lanes.
     if (lane == 0) {
       prefetch_tensormap(&k8_map);
-      prefetch_tensormap(&blocks_map);
+      prefetch_tensormap(&page_map);
+      prefetch_tensormap(&half_map);
     }
     // pages are read by both CTAs of the pair (the second time from L2)
     const uint64_t policy = l2_evict_normal_policy();
     const float *scales = k_scale + int64_t(kvh) * scale_head;
-    const bool prefetch = p.h_kv == 1;
-    Groups wa, wb, wf;  // own pages, partner value halves, L2 prefetch ahead of the own pages
+    Groups wa, wb;  // own pages, partner value halves
     wa.start(p, pc, prow0);
     wb = wa;
-    wf = wa;
-    if (prefetch)  // the first loads go to the ring and the query alone
-      for (int i = 0; i < 2 * T::kStages && !wf.done; ++i) wf.next(p, pc, prow0);
     bool ok = true;
     unsigned long long idle_since = 0;
     uint32_t spins = 0;
@@ -393,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
         wb.pages(p, pa, pb);
         if (lane == 0) {
           if (leader) mbar_arrive_expect_tx(bar(T::VFULL + wb.stage), 2 * T::kHalfVBytes);
-          load_blocks_for_pair(slot(wb.stage, leader ? 2 : 0), &blocks_map, bar_cta0(T::VFULL + wb.stage),
+          load_blocks_for_pair(slot(wb.stage, leader ? 2 : 0), &half_map, bar_cta0(T::VFULL + wb.stage),
                                (leader ? pb : pa) * kPage, kvh, leader ? 0 : 1, policy);
         }
         __syncwarp();
@@ -411,22 +406,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
           mbar_arrive_expect_tx(bar(T::SCALES + st), 512);
         }
         __syncwarp();
-        if (lane < 2)
-          load_blocks_for_pair(slot(st, 2 * lane), &blocks_map, bar_cta0(T::FULL + st), phys * kPage, kvh, lane, policy);
-        else if (lane == 2)
+        if (lane == 0)
+          load_blocks_for_pair(slot(st, 0), &page_map, bar_cta0(T::FULL + st), phys * kPage, kvh, 0, policy);
+        else if (lane == 1)
           load_for_pair(slot(st, 4), &k8_map, bar_cta0(T::FULL + st), 512, kvh, phys * kPage, policy);
-        else if (lane < 5)
-          bulk_load_hint(sbase + T::kOffSc + st * 512 + (lane - 3) * 256, scales + int64_t(lane == 3 ? pa : pb) * kPage, 256,
+        else if (lane < 4)
+          bulk_load_hint(sbase + T::kOffSc + st * 512 + (lane - 2) * 256, scales + int64_t(lane == 2 ? pa : pb) * kPage, 256,
                          bar(T::SCALES + st), policy);
         __syncwarp();
-        if (prefetch && wa.count >= T::kStages && !wf.done) {
-          int fa, fb;
-          wf.pages(p, fa, fb);
-          if (lane == 0)
-            prefetch_l2_bulk(p.kv_base + int64_t(leader ? fa : fb) * kPage * p.kv_token_bytes, kPage * kD);
-          __syncwarp();
-          wf.next(p, pc, prow0);
-        }
         wa.next(p, pc, prow0);
         progressed = true;
       }
@@ -884,14 +871,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
   pair_sync();
 }
 
-cudaError_t launch_decode_fp8_pair(const CUtensorMap &k8_map, const CUtensorMap &blocks_map, const DecodeParams &p, const float *k_scale,
+cudaError_t launch_decode_fp8_pair(const CUtensorMap &k8_map, const CUtensorMap &page_map, const CUtensorMap &half_map, const DecodeParams &p, const float *k_scale,
                                    int64_t num_pages, cudaStream_t stream) {
   using T = FpPair;
   cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_fp8_pair_kernel), T::kSmemBytes);
   if (e != cudaSuccess) return e;
   const unsigned pairs = unsigned((p.R + 2 * T::BM - 1) / (2 * T::BM));
   return launch_early(decode_fp8_pair_kernel, dim3(2 * pairs, p.num_parts, p.h_kv), dim3(T::kThreads), T::kSmemBytes,
-                      stream, k8_map, blocks_map, p, k_scale, num_pages * kPage);
+                      stream, k8_map, page_map, half_map, p, k_scale, num_pages * kPage);
 }
 
 }  // namespace pagedmla

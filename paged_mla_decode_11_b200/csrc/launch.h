@@ -42,8 +42,8 @@ cudaError_t launch_decode_tc_narrow(const CUtensorMap &kv_map, const CUtensorMap
 cudaError_t launch_decode_fp8(const CUtensorMap &k8_map, const CUtensorMap &scale_map, const CUtensorMap &q_map,
                               const DecodeParams &p, cudaStream_t stream);
 // The CTA-pair kernel over the FP8 cache, any number of query rows per latent head.
-cudaError_t launch_decode_fp8_pair(const CUtensorMap &k8_map, const CUtensorMap &blocks_map, const DecodeParams &p,
-                                   const float *k_scale, int64_t num_pages, cudaStream_t stream);
+cudaError_t launch_decode_fp8_pair(const CUtensorMap &k8_map, const CUtensorMap &page_map, const CUtensorMap &half_map,
+                                   const DecodeParams &p, const float *k_scale, int64_t num_pages, cudaStream_t stream);
 cudaError_t launch_combine(const int32_t *num_splits, int batch, int s_q, int h_q, int h_kv,
                            const float *lse_accum, const float *o_accum, __nv_bfloat16 *out,
                            float *lse, cudaStream_t stream, int sq_fold = 1);
