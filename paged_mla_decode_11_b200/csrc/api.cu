@@ -187,7 +187,8 @@ int check_dtype(int dtype) {
 }
 
 int check_rows(int64_t tokens, int h_kv, int64_t num_pages, int page_size) {
-  if (tokens < 0 || h_kv < 1) return fail(MLA_ERR_ARG, "tokens must be >= 0 and h_kv >= 1");
+  if (tokens < 0 || h_kv < 1 || h_kv > 65535)
+    return fail(MLA_ERR_ARG, "tokens must be >= 0 and h_kv in [1, 65535]");
   if (tokens > (int64_t(1) << 31) / h_kv) return fail(MLA_ERR_ARG, "tokens * h_kv must be <= 2^31");
   if (page_size != kPage) return fail(MLA_ERR_UNSUPPORTED, "page_size must be %d (got %d)", kPage, page_size);
   if (num_pages < 1 || num_pages > (int64_t(1) << 25)) return fail(MLA_ERR_ARG, "num_pages must be in [1, 2^25]");

@@ -19,7 +19,10 @@ namespace pagedmla {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxAngles = 1024;  // per block (8 KB of shared memory)
 
-// A row of units: each `unit` is VEC pairs, two accesses of VEC elements.
+// Each unit is VEC pairs, two accesses of VEC elements; a tile has at most kRopeUnits of them a
+// thread.  The units are read first, so that the angles are computed while they are on their way.
+constexpr int kRopeUnits = 1;
+
 template <typename T, bool kHalf, int VEC>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
   __shared__ float2 cs[kRopeMaxAngles];
@@ -31,15 +34,33 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const int front = p.width - 2 * n;  // columns that pass through
   grid_launch_dependents();
   grid_dependency_wait();
-  for (int i = threadIdx.x; i < nt * n; i += kRopeThreads)
-    cs[i] = rope_cos_sin(load_position(p.positions, p.pos64, t0 + i / n), __ldg(p.inv_freq + i % n), p.magnitude,
-                         p.inverse);
   const T *x = static_cast<const T *>(p.x);
   T *out = static_cast<T *>(p.out);
+  const int total = nt * nh * units;
+  V a[kRopeUnits], b[kRopeUnits];
+  auto place = [&](int i, int &lt, int &h, int &u, int &c0, int &c1) {
+    const int r = i / units;
+    u = i - r * units;
+    lt = r / nh;
+    h = h0 + r - lt * nh;
+    c0 = front + (kHalf ? u * VEC : 2 * u * VEC);
+    c1 = kHalf ? c0 + n : c0 + VEC;
+  };
+#pragma unroll
+  for (int k = 0; k < kRopeUnits; ++k) {
+    const int i = threadIdx.x + k * kRopeThreads;
+    if (i < total) {
+      int lt, h, u, c0, c1;
+      place(i, lt, h, u, c0, c1);
+      const T *src = x + (t0 + lt) * p.x_t + h * p.x_h;
+      a[k] = load_cg(reinterpret_cast<const V *>(src + c0));
+      b[k] = load_cg(reinterpret_cast<const V *>(src + c1));
+    }
+  }
   if (p.copy_front) {
-    const int fv = front / VEC, total = nt * nh * fv;
+    const int fv = front / VEC, all = nt * nh * fv;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < total; i += kRopeThreads) {
+    for (int i = threadIdx.x; i < all; i += kRopeThreads) {
       const int r = i / fv, c = (i - r * fv) * VEC;
       const int64_t t = t0 + r / nh;
       const int h = h0 + r % nh;
@@ -47,28 +68,29 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
           load_cg(reinterpret_cast<const V *>(x + t * p.x_t + h * p.x_h + c));
     }
   }
+  for (int i = threadIdx.x; i < nt * n; i += kRopeThreads)
+    cs[i] = rope_cos_sin(load_position(p.positions, p.pos64, t0 + i / n), rope_turns(__ldg(p.inv_freq + i % n)),
+                         p.magnitude, p.inverse);
   __syncthreads();
-  const int total = nt * nh * units;
-#pragma unroll 2
-  for (int i = threadIdx.x; i < total; i += kRopeThreads) {
-    const int r = i / units, u = i - r * units, lt = r / nh;
-    const int h = h0 + r - lt * nh;
-    const T *src = x + (t0 + lt) * p.x_t + h * p.x_h + front;
-    T *dst = out + (t0 + lt) * p.o_t + h * p.o_h + front;
-    const int c0 = kHalf ? u * VEC : 2 * u * VEC, c1 = kHalf ? n + u * VEC : c0 + VEC;
-    V a = load_cg(reinterpret_cast<const V *>(src + c0)), b = load_cg(reinterpret_cast<const V *>(src + c1));
+#pragma unroll
+  for (int k = 0; k < kRopeUnits; ++k) {
+    const int i = threadIdx.x + k * kRopeThreads;
+    if (i >= total) break;
+    int lt, h, u, c0, c1;
+    place(i, lt, h, u, c0, c1);
     const float2 *w = cs + lt * n + u * VEC;
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      // pair k of the unit: members a[k], b[k], or neighbours of the 2 VEC columns of a and b
-      T &m0 = kHalf ? a.v[k] : (2 * k < VEC ? a.v[2 * k] : b.v[2 * k - VEC]);
-      T &m1 = kHalf ? b.v[k] : (2 * k + 1 < VEC ? a.v[2 * k + 1] : b.v[2 * k + 1 - VEC]);
+    for (int j = 0; j < VEC; ++j) {
+      // pair j of the unit: members a[j], b[j], or neighbours of the 2 VEC columns of a and b
+      T &m0 = kHalf ? a[k].v[j] : (2 * j < VEC ? a[k].v[2 * j] : b[k].v[2 * j - VEC]);
+      T &m1 = kHalf ? b[k].v[j] : (2 * j + 1 < VEC ? a[k].v[2 * j + 1] : b[k].v[2 * j + 1 - VEC]);
       const float x0 = to_float(m0), x1 = to_float(m1);
-      m0 = from_float<T>(x0 * w[k].x - x1 * w[k].y);
-      m1 = from_float<T>(x0 * w[k].y + x1 * w[k].x);
+      m0 = from_float<T>(x0 * w[j].x - x1 * w[j].y);
+      m1 = from_float<T>(x0 * w[j].y + x1 * w[j].x);
     }
-    *reinterpret_cast<V *>(dst + c0) = a;
-    *reinterpret_cast<V *>(dst + c1) = b;
+    T *dst = out + (t0 + lt) * p.o_t + h * p.o_h;
+    *reinterpret_cast<V *>(dst + c0) = a[k];
+    *reinterpret_cast<V *>(dst + c1) = b[k];
   }
 }
 
@@ -87,9 +109,9 @@ cudaError_t launch_rope(RopeParams p, int dtype, bool half, cudaStream_t stream)
   const bool wide = multiple(p.pairs) && multiple(p.width) && multiple(p.x_t) && multiple(p.x_h) && multiple(p.o_t) &&
                     multiple(p.o_h) && reinterpret_cast<uintptr_t>(p.x) % 16 == 0 &&
                     reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
-  // about two units a thread: enough bytes in flight, and enough blocks for small calls
+  // a tile of heads, then of tokens, of at most kRopeUnits units a thread (pairs <= 512 fit alone)
   const int units = wide ? p.pairs / vec : p.pairs;
-  const int target = 2 * kRopeThreads;
+  const int target = kRopeUnits * kRopeThreads;
   p.tile_heads = std::max(1, std::min(p.heads, target / units));
   p.tile_tokens = std::max(1, std::min(target / (units * p.tile_heads), kRopeMaxAngles / p.pairs));
   switch (dtype) {

@@ -8,14 +8,19 @@
 
 namespace pagedmla {
 
-// (cos, sin) of position * inv_freq, times the magnitude.  The turns are counted and reduced in
+// A pair's frequency in turns per position.
+__device__ __forceinline__ double rope_turns(double inv_freq) { return inv_freq * 0.15915494309189533577; }  // 1 / (2 pi)
+
+// (cos, sin) of position * frequency, times the magnitude.  The turns are counted and reduced in
 // fp64: at position 10^6 the angle of the fastest pair is 10^6 radians, and an fp32 product would
 // be off by up to 0.03.  The reduced half turn in [-1, 1] goes to sincospif, so the angle's total
-// error stays near 10^-7 at any position.
-__device__ __forceinline__ float2 rope_cos_sin(double position, double inv_freq, float magnitude, bool inverse) {
-  const double turns = position * (inv_freq * 0.15915494309189533577);  // 1 / (2 pi)
+// error stays near 10^-7 at any position (of up to 2^50 turns).
+__device__ __forceinline__ float2 rope_cos_sin(double position, double turns_per_position, float magnitude, bool inverse) {
+  const double turns = position * turns_per_position;
+  constexpr double kRound = 6755399441055744.0;  // 1.5 * 2^52: adding it rounds to a whole number
+  const double whole = __dadd_rn(__dadd_rn(turns, kRound), -kRound);
   float s, c;
-  sincospif(float(2.0 * (turns - rint(turns))), &s, &c);
+  sincospif(2.f * float(turns - whole), &s, &c);
   s *= magnitude;
   return make_float2(c * magnitude, inverse ? -s : s);
 }
@@ -68,6 +73,22 @@ __device__ __forceinline__ V load_cg(const V *ptr) {
   using W = typename WordOf<sizeof(V)>::type;
   const W w = __ldcg(reinterpret_cast<const W *>(ptr));
   return *reinterpret_cast<const V *>(&w);
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+  return d;
 }
 
 }  // namespace pagedmla

@@ -11,8 +11,9 @@
 // Only the sampled row of p and of q is read in full, once, so HBM bounds large batches and the
 // latency of a few dependent reads small ones.  A cluster of CTAs takes a sequence: each CTA a
 // contiguous range of the vocabulary, each of its warps a contiguous segment.  The segments'
-// sums are exchanged through distributed shared memory, every CTA finds the segment that holds
-// the wanted point, and the CTA that owns it reads it again (from L2) and scans it.  Sums are
+// sums go to every CTA of the cluster through distributed shared memory, every CTA finds the
+// segment that holds the wanted point, and the CTA that owns it reads it again (from L2) and
+// scans it.  Sums are
 // fp64: a point of the distribution falls between running sums 1/V apart, and fp32 sums over
 // 10^5 entries are off by a good part of that.  The order of the sums is fixed by the launch
 // shape, without atomics.
@@ -47,17 +48,20 @@ __device__ __forceinline__ double warp_scan(double v, int lane) {
   return v;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p) {
+// VEC: elements of an access (16 bytes when rows and strides allow it, else one).
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyParams p) {
   namespace cg = cooperative_groups;
+  using V = Pack<T, VEC>;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
   const int seq = blockIdx.x / C, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  __shared__ double seg_sum[kVerifyWarps];                       // read by the whole cluster
-  __shared__ double all_sum[kVerifyMaxCluster * kVerifyWarps];
+  // the segments' sums, written by the whole cluster; a second set for the draw from p itself
+  __shared__ double all_sum[2][kVerifyMaxCluster * kVerifyWarps];
   __shared__ double warp_total[kVerifyWarps];
   __shared__ double s_before, s_point;
   __shared__ int s_accepted, s_segment, s_found, s_last;
+  cluster.barrier_arrive();  // waited for before the first write to another CTA's shared memory
   grid_launch_dependents();
   grid_dependency_wait();
 
@@ -72,11 +76,12 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
       bool good = true;
       if (i < n) {
         const int tok = __ldcg(tokens + i);
+        const double u = __ldcg(p.uniform + int64_t(seq) * p.drafts + i);
         good = false;
         if (tok >= 0 && tok < p.vocab) {
           const double pt = to_float(load_cg(target + i * p.t_s + tok));
           const double qt = draft ? double(to_float(load_cg(draft + i * p.d_s + tok))) : 1.0;
-          good = double(__ldcg(p.uniform + int64_t(seq) * p.drafts + i)) * qt < pt;
+          good = u * qt < pt;
         }
       }
       const unsigned bad = __ballot_sync(0xffffffffu, !good);
@@ -94,31 +99,43 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
   const int sure = r < n && !draft ? __ldcg(tokens + r) : -1;  // q = 1 at this token
 
   // segment g = rank * kVerifyWarps + warp covers columns [g * len, (g + 1) * len)
-  const int len = (p.vocab + C * kVerifyWarps - 1) / (C * kVerifyWarps);
+  const int segments = C * kVerifyWarps;
+  const int len = ((p.vocab + segments - 1) / segments + VEC - 1) / VEC * VEC;
+  auto begin_of = [&](int g) { return int(min(int64_t(g) * len, int64_t(p.vocab))); };
   bool subtract = r < n;
-  for (;;) {
-    const int64_t lo64 = int64_t(rank * kVerifyWarps + warp) * len;
-    const int lo = int(min(lo64, int64_t(p.vocab))), hi = min(lo + len, p.vocab);
+  for (int round = 0;; ++round) {
+    const int lo = begin_of(rank * kVerifyWarps + warp), hi = begin_of(rank * kVerifyWarps + warp + 1);
     double sum = 0.0;
+    const int whole = lo + (hi - lo) / VEC * VEC;
     if (subtract && qrow) {
-#pragma unroll 8
-      for (int j = lo + lane; j < hi; j += 32) sum += verify_weight(to_float(load_cg(prow + j)), to_float(load_cg(qrow + j)));
+#pragma unroll 4
+      for (int j = lo + lane * VEC; j < whole; j += 32 * VEC) {
+        const V a = load_cg(reinterpret_cast<const V *>(prow + j)), b = load_cg(reinterpret_cast<const V *>(qrow + j));
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) sum += verify_weight(to_float(a.v[k]), to_float(b.v[k]));
+      }
     } else {
-#pragma unroll 8
-      for (int j = lo + lane; j < hi; j += 32)
-        sum += verify_weight(to_float(load_cg(prow + j)), subtract && j == sure ? 1.f : 0.f);
+#pragma unroll 4
+      for (int j = lo + lane * VEC; j < whole; j += 32 * VEC) {
+        const V a = load_cg(reinterpret_cast<const V *>(prow + j));
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) sum += verify_weight(to_float(a.v[k]), subtract && j + k == sure ? 1.f : 0.f);
+      }
     }
+    auto weight_at = [&](int j) {
+      const float q = !subtract ? 0.f : qrow ? to_float(load_cg(qrow + j)) : (j == sure ? 1.f : 0.f);
+      return verify_weight(to_float(load_cg(prow + j)), q);
+    };
+    if (VEC > 1 && whole + lane < hi) sum += weight_at(whole + lane);  // the row's last few
     sum = warp_sum(sum);
-    if (lane == 0) seg_sum[warp] = sum;
+    if (round == 0) cluster.barrier_wait();
+    if (lane < C) *cluster.map_shared_rank(&all_sum[round][rank * kVerifyWarps + warp], lane) = sum;
     cluster.sync();
-    for (int i = tid; i < C * kVerifyWarps; i += kVerifyThreads)
-      all_sum[i] = *cluster.map_shared_rank(&seg_sum[i % kVerifyWarps], i / kVerifyWarps);
-    cluster.sync();  // no CTA rewrites or leaves seg_sum while another reads it
     if (warp == 0) {
-      // lane l takes C * 16 / 32 consecutive segments, an odd C leaves the last lanes without any
-      const int per = (C * kVerifyWarps + 31) / 32, g0 = lane * per, g1 = min(g0 + per, C * kVerifyWarps);
+      const double *sums = all_sum[round];
+      const int per = (segments + 31) / 32, g0 = min(lane * per, segments), g1 = min(g0 + per, segments);
       double mine = 0.0;
-      for (int g = g0; g < g1; ++g) mine += all_sum[g];
+      for (int g = g0; g < g1; ++g) mine += sums[g];
       const double upto = warp_scan(mine, lane);
       const double total = __shfl_sync(0xffffffffu, upto, 31);
       const double u = fmax(double(__ldcg(p.uniform_new + seq)), 0.0);
@@ -128,8 +145,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
       int seg = 0x7fffffff, last = -1;
       double before = 0.0, run = upto - mine;
       for (int g = g0; g < g1; ++g) {
-        const double next = run + all_sum[g];
-        if (all_sum[g] > 0.0) {
+        const double next = run + sums[g];
+        if (sums[g] > 0.0) {
           last = g;
           if (seg == 0x7fffffff && next > point) {
             seg = g;
@@ -151,57 +168,61 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         s_point = INFINITY;
       }
     }
+    if (tid == 32) {
+      s_found = 0x7fffffff;
+      s_last = -1;
+    }
     __syncthreads();
-    if (s_segment >= 0 || !subtract) break;
+    if (s_segment >= 0 || !subtract) {
+      const int seg = s_segment;
+      if (seg >= 0 ? seg / kVerifyWarps != rank : rank != 0) return;
+      int token = -1;
+      if (seg >= 0) {
+        // four neighbouring columns a thread
+        const int end = begin_of(seg + 1);
+        const double point = s_point;
+        double base = s_before;
+        for (int j0 = begin_of(seg); j0 < end; j0 += 4 * kVerifyThreads) {
+          const int j = j0 + 4 * tid;
+          double w[4], c = 0.0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = j + k < end ? weight_at(j + k) : 0.0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) c += w[k];
+          const double upto = warp_scan(c, lane);
+          if (lane == 31) warp_total[warp] = upto;
+          __syncthreads();
+          double off = base;
+          for (int k = 0; k < warp; ++k) off += warp_total[k];
+          double run = off + (upto - c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            run += w[k];
+            if (w[k] > 0.0) {
+              if (run > point) atomicMin(&s_found, j + k);
+              atomicMax(&s_last, j + k);
+            }
+          }
+          for (int k = warp; k < kVerifyWarps; ++k) off += warp_total[k];
+          base = off;
+          __syncthreads();
+          if (s_found != 0x7fffffff) break;
+        }
+        // rounding may leave the scan a little short of the segment's sum: its last token then
+        token = s_found != 0x7fffffff ? s_found : s_last;
+      }
+      for (int i = tid; i <= p.drafts; i += kVerifyThreads)
+        p.out[int64_t(seq) * (p.drafts + 1) + i] = i < r ? __ldcg(tokens + i) : i == r ? token : -1;
+      if (tid == 0) p.accepted[seq] = r;
+      return;
+    }
     subtract = false;  // p <= q everywhere (rounded rows): draw from p itself
     __syncthreads();
   }
-
-  const int seg = s_segment;
-  if (seg >= 0 ? seg / kVerifyWarps == rank : rank == 0) {
-    int token = -1;
-    if (seg >= 0) {
-      const int lo = int(min(int64_t(seg) * len, int64_t(p.vocab))), hi = min(lo + len, p.vocab);
-      const double point = s_point;
-      double base = s_before;
-      if (tid == 0) {
-        s_found = 0x7fffffff;
-        s_last = -1;
-      }
-      for (int j0 = lo; j0 < hi; j0 += kVerifyThreads) {
-        const int j = j0 + tid;
-        double w = 0.0;
-        if (j < hi) {
-          const float q = !subtract ? 0.f : qrow ? to_float(load_cg(qrow + j)) : (j == sure ? 1.f : 0.f);
-          w = verify_weight(to_float(load_cg(prow + j)), q);
-        }
-        double c = warp_scan(w, lane);
-        if (lane == 31) warp_total[warp] = c;
-        __syncthreads();
-        double off = base;
-        for (int k = 0; k < warp; ++k) off += warp_total[k];
-        c += off;
-        if (w > 0.0) {
-          if (c > point) atomicMin(&s_found, j);
-          atomicMax(&s_last, j);
-        }
-        for (int k = warp; k < kVerifyWarps; ++k) off += warp_total[k];
-        base = off;
-        __syncthreads();
-        if (s_found != 0x7fffffff) break;
-      }
-      __syncthreads();
-      // rounding may leave the scan a little short of the segment's sum: its last token then
-      token = s_found != 0x7fffffff ? s_found : s_last;
-    }
-    for (int i = tid; i <= p.drafts; i += kVerifyThreads)
-      p.out[int64_t(seq) * (p.drafts + 1) + i] = i < r ? __ldcg(tokens + i) : i == r ? token : -1;
-    if (tid == 0) p.accepted[seq] = r;
-  }
 }
 
-template <typename T>
-static cudaError_t launch_verify_typed(const VerifyParams &p, cudaStream_t stream) {
+template <typename T, int VEC>
+static cudaError_t launch_verify_vec(const VerifyParams &p, cudaStream_t stream) {
   int C = kVerifyMaxCluster;
   while (C > 1 && int64_t(p.batch) * C > 296) C /= 2;
   cudaLaunchConfig_t cfg = {};
@@ -216,7 +237,15 @@ static cudaError_t launch_verify_typed(const VerifyParams &p, cudaStream_t strea
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<T>, p);
+  return cudaLaunchKernelEx(&cfg, verify_kernel<T, VEC>, p);
+}
+
+template <typename T>
+static cudaError_t launch_verify_typed(const VerifyParams &p, cudaStream_t stream) {
+  constexpr int kVec = 16 / sizeof(T);
+  const bool wide = reinterpret_cast<uintptr_t>(p.target) % 16 == 0 && reinterpret_cast<uintptr_t>(p.draft) % 16 == 0 &&
+                    p.t_b % kVec == 0 && p.t_s % kVec == 0 && p.d_b % kVec == 0 && p.d_s % kVec == 0;
+  return wide ? launch_verify_vec<T, kVec>(p, stream) : launch_verify_vec<T, 1>(p, stream);
 }
 
 cudaError_t launch_verify(const VerifyParams &p, int dtype, cudaStream_t stream) {
