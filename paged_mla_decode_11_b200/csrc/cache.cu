@@ -67,7 +67,7 @@ cudaError_t launch_cache_slots(const int32_t *row_ptr, const int32_t *seqlens, i
 // two to an instruction; and a row is divided by its scale with one division (below).
 // ------------------------------------------------------------------------------------
 constexpr int kWriteWarps = 4, kWriteBlocks = 7;  // warps a block, blocks an SM
-constexpr int kWriteAhead = 4;                     // rows of a warp in shared memory
+constexpr int kWriteAhead = 3;                     // rows of a warp in shared memory
 
 __device__ __forceinline__ uint32_t e4m3x2(float2 v) { return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3); }
 

@@ -64,8 +64,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       const int r = i / fv, c = (i - r * fv) * VEC;
       const int64_t t = t0 + r / nh;
       const int h = h0 + r % nh;
-      *reinterpret_cast<V *>(out + t * p.o_t + h * p.o_h + c) =
-          load_cg(reinterpret_cast<const V *>(x + t * p.x_t + h * p.x_h + c));
+      store_cs(reinterpret_cast<V *>(out + t * p.o_t + h * p.o_h + c),
+               load_cg(reinterpret_cast<const V *>(x + t * p.x_t + h * p.x_h + c)));
     }
   }
   for (int i = threadIdx.x; i < nt * n; i += kRopeThreads)
@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       m1 = from_float<T>(x0 * w[j].y + x1 * w[j].x);
     }
     T *dst = out + (t0 + lt) * p.o_t + h * p.o_h;
-    *reinterpret_cast<V *>(dst + c0) = a[k];
-    *reinterpret_cast<V *>(dst + c1) = b[k];
+    store_cs(reinterpret_cast<V *>(dst + c0), a[k]);
+    store_cs(reinterpret_cast<V *>(dst + c1), b[k]);
   }
 }
 

@@ -75,6 +75,14 @@ __device__ __forceinline__ V load_cg(const V *ptr) {
   return *reinterpret_cast<const V *>(&w);
 }
 
+// The same as a streaming store (evicted from L2 first): results larger than L2 then do not push out
+// inputs that are still to be read.
+template <typename V>
+__device__ __forceinline__ void store_cs(V *ptr, const V &v) {
+  using W = typename WordOf<sizeof(V)>::type;
+  __stcs(reinterpret_cast<W *>(ptr), *reinterpret_cast<const W *>(&v));
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;

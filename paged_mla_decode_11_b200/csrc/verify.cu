@@ -25,6 +25,7 @@
 namespace pagedmla {
 
 constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32, kVerifyMaxCluster = 8;
+constexpr int kVerifyAhead = 4;  // 512-byte pieces of a warp's rows on their way
 
 // The weight of a token; what is not a finite positive number has none.
 __device__ __forceinline__ double verify_weight(float p, float q) {
@@ -48,7 +49,57 @@ __device__ __forceinline__ double warp_scan(double v, int lane) {
   return v;
 }
 
-// VEC: elements of an access (16 bytes when rows and strides allow it, else one).
+struct SegmentAt {
+  int segment;    // -1: nothing has weight
+  double before;  // running sum in front of it
+  double point;   // what the running sum has to exceed
+};
+
+// The segment that holds the wanted point, found by one warp: lane l sums `per` neighbouring segments;
+// the first lane whose running sum exceeds the point has it.  A point at or past the total (u' of 1 or
+// more) takes the last segment that holds anything.
+__device__ __forceinline__ SegmentAt find_segment(const double *sums, int segments, float uniform, int lane) {
+  const int per = (segments + 31) / 32, g0 = min(lane * per, segments), g1 = min(g0 + per, segments);
+  double mine = 0.0;
+#pragma unroll 1
+  for (int g = g0; g < g1; ++g) mine += sums[g];
+  const double upto = warp_scan(mine, lane);
+  const double point = double(uniform) * __shfl_sync(0xffffffffu, upto, 31);
+  const unsigned some = __ballot_sync(0xffffffffu, mine > 0.0), over = __ballot_sync(0xffffffffu, mine > 0.0 && upto > point);
+  SegmentAt at = {-1, 0.0, over ? point : INFINITY};
+  if (some == 0) return at;
+  const int from = over ? __ffs(over) - 1 : 31 - __clz(some);
+  double run = __shfl_sync(0xffffffffu, upto - mine, from);
+#pragma unroll 1
+  for (int g = from * per; g < min(from * per + per, segments); ++g) {
+    const double w = sums[g];
+    if (w > 0.0) {
+      at.segment = g;
+      at.before = run;
+      if (run + w > point) break;
+    }
+    run += w;
+  }
+  return at;
+}
+
+// Store 8 bytes at the same place of CTA `rank` of the cluster, counted by its barrier.
+__device__ __forceinline__ void send_to_cta(double value, uint32_t local, uint32_t barrier, int rank) {
+  uint32_t at, bar;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(local), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(barrier), "r"(rank));
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(at),
+               "l"(__double_as_longlong(value)), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void verify_copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// VEC: elements of an access.  16 bytes when rows and strides allow it: these go through a ring in
+// shared memory (cp.async), deep enough to keep HBM busy with few registers; every lane reads back
+// what it copied itself.  Otherwise one element at a time.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyParams p) {
   namespace cg = cooperative_groups;
@@ -56,25 +107,42 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
   cg::cluster_group cluster = cg::this_cluster();
   const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
   const int seq = blockIdx.x / C, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  // the segments' sums, written by the whole cluster; a second set for the draw from p itself
+  extern __shared__ __align__(16) uint8_t verify_ring[];
+  // The segments' sums of the whole cluster, and of this CTA; a second set for the draw from p itself.
+  // They are exchanged by counted stores that only warp 0 waits for: a cluster barrier in their place
+  // makes every warp acquire at cluster scope, after which the SM's shuffles took 250 cycles each.
   __shared__ double all_sum[2][kVerifyMaxCluster * kVerifyWarps];
+  __shared__ double own_sum[kVerifyWarps];
+  __shared__ uint64_t s_full[2];
+  __shared__ int s_abort;
   __shared__ double warp_total[kVerifyWarps];
   __shared__ double s_before, s_point;
+  __shared__ float s_uniform;
   __shared__ int s_accepted, s_segment, s_found, s_last;
-  cluster.barrier_arrive();  // waited for before the first write to another CTA's shared memory
+  if (tid == 0) {
+    s_abort = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_arrive_expect_tx(smem_u32(&s_full[i]), uint32_t(C * kVerifyWarps * sizeof(double)));
+    }
+    fence_barrier_init();
+  }
+  cluster.barrier_arrive();  // every CTA's barriers are ready before a store to it
   grid_launch_dependents();
   grid_dependency_wait();
 
-  const int n = max(0, min(p.num_drafts ? __ldcg(p.num_drafts + seq) : p.drafts, p.drafts));
+  // What needs no other value first is read at once: the drafts' probabilities are the second round
+  // trip to memory, the sampled row the third.
+  int n = p.num_drafts ? __ldcg(p.num_drafts + seq) : p.drafts;
   const T *target = static_cast<const T *>(p.target) + seq * p.t_b;
   const T *draft = p.draft ? static_cast<const T *>(p.draft) + seq * p.d_b : nullptr;
   const int32_t *tokens = p.tokens + int64_t(seq) * p.drafts;
   if (warp == 0) {
     int r = 0;
-    for (; r < n; r += 32) {
+    for (;; r += 32) {
       const int i = r + lane;
       bool good = true;
-      if (i < n) {
+      if (i < p.drafts) {
         const int tok = __ldcg(tokens + i);
         const double u = __ldcg(p.uniform + int64_t(seq) * p.drafts + i);
         good = false;
@@ -84,15 +152,21 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
           good = u * qt < pt;
         }
       }
-      const unsigned bad = __ballot_sync(0xffffffffu, !good);
+      const unsigned bad = __ballot_sync(0xffffffffu, !good || i >= min(n, p.drafts));  // the n-th place ends it
       if (bad) {
         r += __ffs(bad) - 1;
         break;
       }
     }
-    if (lane == 0) s_accepted = min(r, n);
+    if (lane == 0) s_accepted = r;
+  } else if (tid == 32) {
+    s_uniform = fmaxf(__ldcg(p.uniform_new + seq), 0.f);
+    s_found = 0x7fffffff;
+    s_last = -1;
   }
+  cluster.barrier_wait();
   __syncthreads();
+  n = max(0, min(n, p.drafts));
   const int r = s_accepted;
   const T *prow = target + r * p.t_s;
   const T *qrow = r < n && draft ? draft + r * p.d_s : nullptr;
@@ -105,115 +179,119 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
   bool subtract = r < n;
   for (int round = 0;; ++round) {
     const int lo = begin_of(rank * kVerifyWarps + warp), hi = begin_of(rank * kVerifyWarps + warp + 1);
+    const bool both = subtract && qrow;
+    const int one_at = subtract ? sure : -1;
+    auto weight_at = [&](int j) {
+      return verify_weight(to_float(load_cg(prow + j)), both ? to_float(load_cg(qrow + j)) : j == one_at ? 1.f : 0.f);
+    };
+    // A lane's sum: conversions to fp64 run at a sixteenth of the fp32 rate, so only the rounded
+    // difference d of p > q is converted; the rest of it, (p - d) - q, is exact in fp32 and below 2^-24 d,
+    // and an fp32 sum of the rests is off by less than 2^-43 of the whole.
     double sum = 0.0;
-    const int whole = lo + (hi - lo) / VEC * VEC;
-    if (subtract && qrow) {
-#pragma unroll 4
+    float rest = 0.f;
+    auto add = [&](float pj, float qj) {
+      const float d = pj - qj;
+      const bool some = d > 0.f && d <= 3.402823466e38f;
+      sum += double(some ? d : 0.f);
+      rest += some ? (pj - d) - qj : 0.f;
+    };
+    if constexpr (VEC > 1) {
+      uint8_t *ring = verify_ring + (warp * kVerifyAhead * 2 * 32 + lane) * 16;
+      const uint32_t ring_at = smem_u32(ring);
+      const int whole = lo + (hi - lo) / VEC * VEC;
+      int next = lo + lane * VEC;  // column of the next copy
+      auto copy = [&](int stage) {
+        if (next < whole) {
+          verify_copy16(ring_at + stage * 1024, prow + next);
+          if (both) verify_copy16(ring_at + stage * 1024 + 512, qrow + next);
+          next += 32 * VEC;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll 1
+      for (int i = 0; i < kVerifyAhead - 1; ++i) copy(i);
+      int stage = 0;
+#pragma unroll 1
       for (int j = lo + lane * VEC; j < whole; j += 32 * VEC) {
-        const V a = load_cg(reinterpret_cast<const V *>(prow + j)), b = load_cg(reinterpret_cast<const V *>(qrow + j));
+        copy(stage == 0 ? kVerifyAhead - 1 : stage - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kVerifyAhead - 1) : "memory");
+        const V a = *reinterpret_cast<const V *>(ring + stage * 1024);
+        V b{};
+        if (both) b = *reinterpret_cast<const V *>(ring + stage * 1024 + 512);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) sum += verify_weight(to_float(a.v[k]), to_float(b.v[k]));
+        for (int k = 0; k < VEC; ++k) add(to_float(a.v[k]), j + k == one_at ? 1.f : to_float(b.v[k]));
+        stage = stage + 1 == kVerifyAhead ? 0 : stage + 1;
       }
+      if (whole + lane < hi) sum += weight_at(whole + lane);  // the row's last few
     } else {
 #pragma unroll 4
-      for (int j = lo + lane * VEC; j < whole; j += 32 * VEC) {
-        const V a = load_cg(reinterpret_cast<const V *>(prow + j));
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) sum += verify_weight(to_float(a.v[k]), subtract && j + k == sure ? 1.f : 0.f);
-      }
+      for (int j = lo + lane; j < hi; j += 32)
+        add(to_float(load_cg(prow + j)), both ? to_float(load_cg(qrow + j)) : j == one_at ? 1.f : 0.f);
     }
-    auto weight_at = [&](int j) {
-      const float q = !subtract ? 0.f : qrow ? to_float(load_cg(qrow + j)) : (j == sure ? 1.f : 0.f);
-      return verify_weight(to_float(load_cg(prow + j)), q);
-    };
-    if (VEC > 1 && whole + lane < hi) sum += weight_at(whole + lane);  // the row's last few
+    sum += double(rest);
     sum = warp_sum(sum);
-    if (round == 0) cluster.barrier_wait();
-    if (lane < C) *cluster.map_shared_rank(&all_sum[round][rank * kVerifyWarps + warp], lane) = sum;
-    cluster.sync();
+    if (lane == 0) own_sum[warp] = sum;
+    __syncthreads();
     if (warp == 0) {
-      const double *sums = all_sum[round];
-      const int per = (segments + 31) / 32, g0 = min(lane * per, segments), g1 = min(g0 + per, segments);
-      double mine = 0.0;
-      for (int g = g0; g < g1; ++g) mine += sums[g];
-      const double upto = warp_scan(mine, lane);
-      const double total = __shfl_sync(0xffffffffu, upto, 31);
-      const double u = fmax(double(__ldcg(p.uniform_new + seq)), 0.0);
-      const double point = u * total;
-      // the first segment whose running sum exceeds the point; a point at or past the total
-      // (u' of 1 or more) takes the last segment that holds anything
-      int seg = 0x7fffffff, last = -1;
-      double before = 0.0, run = upto - mine;
-      for (int g = g0; g < g1; ++g) {
-        const double next = run + sums[g];
-        if (sums[g] > 0.0) {
-          last = g;
-          if (seg == 0x7fffffff && next > point) {
-            seg = g;
-            before = run;
-          }
-        }
-        run = next;
+      const uint32_t full = smem_u32(&s_full[round]);
+      for (int i = lane; i < C * kVerifyWarps; i += 32)
+        send_to_cta(own_sum[i % kVerifyWarps], smem_u32(&all_sum[round][rank * kVerifyWarps + i % kVerifyWarps]), full,
+                    i / kVerifyWarps);
+      mbar_wait(full, 0, &s_abort, nullptr, 2000000000ull);
+      __syncwarp();
+      const SegmentAt found = find_segment(all_sum[round], segments, s_uniform, lane);
+      if (lane == 0) {
+        s_segment = found.segment;
+        s_before = found.before;
+        s_point = found.point;
       }
-      const int first = __reduce_min_sync(0xffffffffu, seg), end = __reduce_max_sync(0xffffffffu, last);
-      if (first != 0x7fffffff) {
-        if (seg == first) {
-          s_segment = first;
-          s_before = before;
-          s_point = point;
-        }
-      } else if (lane == 0) {
-        s_segment = end;  // -1: nothing has weight
-        s_before = 0.0;
-        s_point = INFINITY;
-      }
-    }
-    if (tid == 32) {
-      s_found = 0x7fffffff;
-      s_last = -1;
+    } else if (warp == 1 && rank == 0 && round == 0) {
+      // the tokens around the new one, while it is looked for
+      for (int i = lane; i <= p.drafts; i += 32)
+        if (i != r) p.out[int64_t(seq) * (p.drafts + 1) + i] = i < r ? __ldcg(tokens + i) : -1;
+      if (lane == 0) p.accepted[seq] = r;
     }
     __syncthreads();
-    if (s_segment >= 0 || !subtract) {
-      const int seg = s_segment;
-      if (seg >= 0 ? seg / kVerifyWarps != rank : rank != 0) return;
-      int token = -1;
-      if (seg >= 0) {
-        // four neighbouring columns a thread
-        const int end = begin_of(seg + 1);
-        const double point = s_point;
-        double base = s_before;
-        for (int j0 = begin_of(seg); j0 < end; j0 += 4 * kVerifyThreads) {
-          const int j = j0 + 4 * tid;
-          double w[4], c = 0.0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = j + k < end ? weight_at(j + k) : 0.0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) c += w[k];
-          const double upto = warp_scan(c, lane);
-          if (lane == 31) warp_total[warp] = upto;
-          __syncthreads();
-          double off = base;
-          for (int k = 0; k < warp; ++k) off += warp_total[k];
-          double run = off + (upto - c);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            run += w[k];
-            if (w[k] > 0.0) {
-              if (run > point) atomicMin(&s_found, j + k);
-              atomicMax(&s_last, j + k);
-            }
-          }
-          for (int k = warp; k < kVerifyWarps; ++k) off += warp_total[k];
-          base = off;
-          __syncthreads();
-          if (s_found != 0x7fffffff) break;
-        }
-        // rounding may leave the scan a little short of the segment's sum: its last token then
-        token = s_found != 0x7fffffff ? s_found : s_last;
+    const int seg = s_segment;
+    if (seg >= 0 || !subtract) {
+      int32_t *out = p.out + int64_t(seq) * (p.drafts + 1) + r;
+      if (seg < 0) {
+        if (rank == 0 && tid == 0) *out = -1;
+        return;
       }
-      for (int i = tid; i <= p.drafts; i += kVerifyThreads)
-        p.out[int64_t(seq) * (p.drafts + 1) + i] = i < r ? __ldcg(tokens + i) : i == r ? token : -1;
-      if (tid == 0) p.accepted[seq] = r;
+      if (seg / kVerifyWarps != rank) return;
+      // four neighbouring columns a thread
+      const int end = begin_of(seg + 1);
+      const double point = s_point;
+      double base = s_before;
+      for (int j0 = begin_of(seg); j0 < end; j0 += 4 * kVerifyThreads) {
+        const int j = j0 + 4 * tid;
+        double w[4], c = 0.0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = j + k < end ? weight_at(j + k) : 0.0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c += w[k];
+        const double upto = warp_scan(c, lane);
+        if (lane == 31) warp_total[warp] = upto;
+        __syncthreads();
+        double off = base;
+        for (int k = 0; k < warp; ++k) off += warp_total[k];
+        double run = off + (upto - c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          run += w[k];
+          if (w[k] > 0.0) {
+            if (run > point) atomicMin(&s_found, j + k);
+            atomicMax(&s_last, j + k);
+          }
+        }
+        for (int k = warp; k < kVerifyWarps; ++k) off += warp_total[k];
+        base = off;
+        __syncthreads();
+        if (s_found != 0x7fffffff) break;
+      }
+      // rounding may leave the scan a little short of the segment's sum: its last token then
+      if (tid == 0) *out = s_found != 0x7fffffff ? s_found : s_last;
       return;
     }
     subtract = false;  // p <= q everywhere (rounded rows): draw from p itself
@@ -223,11 +301,14 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyP
 
 template <typename T, int VEC>
 static cudaError_t launch_verify_vec(const VerifyParams &p, cudaStream_t stream) {
+  constexpr int kRing = VEC > 1 ? kVerifyWarps * kVerifyAhead * 2 * 512 : 0;
+  if (cudaError_t e = set_smem_once(reinterpret_cast<const void *>(verify_kernel<T, VEC>), kRing)) return e;
   int C = kVerifyMaxCluster;
   while (C > 1 && int64_t(p.batch) * C > 296) C /= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(p.batch * C));
   cfg.blockDim = dim3(kVerifyThreads);
+  cfg.dynamicSmemBytes = kRing;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
