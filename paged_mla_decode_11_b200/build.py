@@ -3,7 +3,9 @@
     python -m paged_mla_decode_11_b200.build [--force]
 
 Each CUDA source is compiled to an object under _build/ and the objects are linked into
-paged_mla_decode_11_b200/libpagedmla.so (CUDA runtime linked statically).
+paged_mla_decode_11_b200/libpagedmla.so (CUDA runtime linked statically).  csrc/binding.cpp,
+the argument marshalling of the per-layer operators, becomes the extension module
+paged_mla_decode_11_b200/_binding.so against the installed torch.
 """
 
 from __future__ import annotations
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedmla.so")
+BINDING = os.path.join(HERE, "_binding.so")
 
 SOURCES = ["api.cu", "metadata.cu", "decode_mma.cu", "decode_tc.cu", "decode_wide.cu", "decode_pair.cu", "decode_fp8.cu", "decode_fp8_pair.cu", "combine.cu", "merge.cu", "absorb.cu", "rope.cu", "cache.cu", "verify.cu", "no_alloc.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -57,14 +61,40 @@ def _compile(src: str, verbose: bool, extra: list[str]) -> str:
     return obj
 
 
+def _build_binding(verbose: bool) -> None:
+    src = os.path.join(CSRC, "binding.cpp")
+    if not _stale(BINDING, [src, os.path.join(INCLUDE, "pagedmla.h")]):
+        return
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", cuda,
+           "-isystem", sysconfig.get_paths()["include"]]
+    for d in cpp_extension.include_paths():
+        cmd += ["-isystem", d]
+    cmd += [src, "-o", tmp, "-ldl"]
+    for d in cpp_extension.library_paths():
+        cmd += ["-L", d]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile every kernel source for sm_100a and link libpagedmla.so; returns its path."""
+    """Compile every kernel source for sm_100a, link libpagedmla.so and build the marshalling
+    module; returns the library's path."""
     extra = list(extra or [])
     os.makedirs(BUILD, exist_ok=True)
     if force:
         for f in os.listdir(BUILD):
             if f.endswith(".o"):
                 os.remove(os.path.join(BUILD, f))
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose, extra), SOURCES))
     if force or _stale(LIB, objs):
@@ -74,6 +104,7 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
+    _build_binding(verbose)
     return LIB
 
 

@@ -3,7 +3,9 @@
 Every step of the decode path runs in the library's CUDA kernels; this module checks
 tensor dtypes, devices and shapes, allocates outputs with torch and passes raw pointers
 and the current CUDA stream.  There is no CPU fallback: without the built library every
-call raises.
+call raises.  The operators called for every layer of a step (rotary positions, cache write
+and read-back, draft verification) do the same in the extension module _binding, where it
+takes a microsecond or two instead of ten.
 
 The call sequence mirrors the pages' FlashMLA usage ("OpenSourceWeek Day 1 - FlashMLA",
 section V.2):
@@ -16,6 +18,7 @@ section V.2):
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 import threading
@@ -46,12 +49,10 @@ EXPORTED = (
     "mla_rope", "mla_cache_slots", "mla_cache_write", "mla_cache_write_fp8", "mla_cache_read", "mla_cache_read_fp8",
     "mla_verify_draft", "mla_decode_paged_fp8_rows",
 )
-MLA_ROPE_HALF = 1
-MLA_ROPE_INVERSE = 2
-MLA_ROPE_POS64 = 4
-DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # MLA_DTYPE_*
+
 
 _lib = None
+_binding = None
 _lib_lock = threading.Lock()
 _I64x3 = ctypes.c_int64 * 3
 
@@ -544,47 +545,19 @@ def absorb_output(o_latent: torch.Tensor, w_uv: torch.Tensor, out: Optional[torc
     return out
 
 
-def _need(t: torch.Tensor, name: str, index: int, dtype: torch.dtype) -> None:
-    """The tensor is of this type and on the CUDA device of that index."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be a CUDA tensor on device {index}")
-
-
-def _cuda_index(t: torch.Tensor, name: str) -> int:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
-
-
-def _raw_stream(index: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
-def _launch(index: int, fn, *args) -> None:
-    """Call a C entry point with the tensors' device current, on its current stream."""
-    if index == torch.cuda.current_device():
-        rc = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, _raw_stream(index))
-    if rc != MLA_OK:
-        _check(rc)
-
-
-def _extent(t: torch.Tensor) -> Tuple[int, int]:
-    last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
-    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
-
-
-def _require_rows_apart(t: torch.Tensor, name: str) -> None:
-    """No element of a [T, H, D] tensor with contiguous rows is reached twice."""
-    need = t.shape[2]
-    for st, n in sorted((st, n) for st, n in zip(t.stride()[:2], t.shape[:2]) if n > 1):
-        if st < need:
-            raise ValueError(f"rows of {name} must not overlap")
-        need += (n - 1) * st
+def load_binding():
+    """The native marshalling of the per-layer operators (csrc/binding.cpp), bound to the loaded
+    library (raises if it is not built).  Shapes, strides and types are checked there."""
+    global _binding
+    if _binding is None:
+        lib = load_library()
+        try:
+            module = importlib.import_module("._binding", __package__)
+        except ModuleNotFoundError:
+            raise ImportError("_binding.so is missing: build it with `python -m paged_mla_decode_11_b200.build`") from None
+        module.bind(lib._handle, MlaError)
+        _binding = module
+    return _binding
 
 
 def rope_frequencies(dim: int = 64, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -633,20 +606,6 @@ def rope_magnitude(factor: float, coefficient: float = 1.0) -> float:
     return 0.1 * coefficient * math.log(factor) + 1.0 if factor > 1.0 else 1.0
 
 
-def _positions_flag(positions: torch.Tensor, tokens: int, index: int) -> int:
-    if positions.dtype == torch.int64:
-        flag = MLA_ROPE_POS64
-    elif positions.dtype == torch.int32:
-        flag = 0
-    else:
-        raise TypeError(f"positions must be int32 or int64 (got {positions.dtype})")
-    if positions.get_device() != index:
-        raise ValueError(f"positions must be a CUDA tensor on device {index}")
-    if positions.shape != (tokens,) or not positions.is_contiguous():
-        raise ValueError("positions must be a contiguous [tokens] tensor")
-    return flag
-
-
 def mla_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool = True,
              magnitude: float = 1.0, inverse: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rotary positions on the last 2 * len(inv_freq) columns of x [T, H, D] (bf16, fp16 or fp32;
@@ -654,38 +613,7 @@ def mla_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, i
     turned by positions[t] * inv_freq[i] (int32 or int64 [T]; fp64 [n], rope_frequencies) and
     multiplied by ``magnitude``; the columns in front are copied.  ``inverse`` turns back, which is
     also the gradient with respect to x.  ``out=x`` works in place."""
-    index = _cuda_index(x, "x")
-    dtype = DTYPES.get(x.dtype)
-    if dtype is None:
-        raise TypeError(f"x must be bf16, fp16 or fp32 (got {x.dtype})")
-    if x.dim() != 3:
-        raise ValueError("x must be [tokens, heads, width]")
-    T, H, D = x.shape
-    xs = x.stride()
-    if xs[2] != 1 and D > 1:
-        raise ValueError("x's last dimension must be contiguous")
-    _need(inv_freq, "inv_freq", index, torch.float64)
-    if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not 1 <= inv_freq.shape[0] <= D // 2:
-        raise ValueError("inv_freq must be a contiguous vector of at most width / 2 frequencies")
-    flags = _positions_flag(positions, T, index) | (0 if interleaved else MLA_ROPE_HALF) | \
-        (MLA_ROPE_INVERSE if inverse else 0)
-    if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    elif out is not x:
-        _need(out, "out", index, x.dtype)
-        if out.shape != x.shape or (out.stride(2) != 1 and D > 1):
-            raise ValueError("out must have x's shape, its last dimension contiguous")
-        if x.numel() and (out.data_ptr() != x.data_ptr() or out.stride() != xs):
-            (a, b), (c, d) = _extent(x), _extent(out)
-            if a < d and c < b:
-                raise ValueError("out must be x itself or must not overlap it")
-    if out.numel() == 0:
-        return out
-    _require_rows_apart(out, "out")
-    os = out.stride()
-    _launch(index, load_library().mla_rope, x.data_ptr(), _I64x2(xs[0], xs[1]), dtype, T, H, D, inv_freq.shape[0],
-            positions.data_ptr(), inv_freq.data_ptr(), magnitude, flags, out.data_ptr(), _I64x2(os[0], os[1]))
-    return out
+    return (_binding or load_binding()).rope(x, positions, inv_freq, interleaved, magnitude, inverse, out)
 
 
 def mla_cache_slots(block_table: torch.Tensor, cache_seqlens: torch.Tensor, row_ptr: torch.Tensor, num_pages: int,
@@ -695,87 +623,7 @@ def mla_cache_slots(block_table: torch.Tensor, cache_seqlens: torch.Tensor, row_
     sequence after sequence by ``row_ptr`` (int32 [b + 1]); those of sequence b are the last of its
     cache_seqlens[b] entries.  Tokens past row_ptr[-1], and any without a page in [0, num_pages),
     get slot -1.  Buffers may be passed for reuse."""
-    index = _cuda_index(block_table, "block_table")
-    _need(block_table, "block_table", index, torch.int32)
-    _need(cache_seqlens, "cache_seqlens", index, torch.int32)
-    _need(row_ptr, "row_ptr", index, torch.int32)
-    if block_table.dim() != 2 or block_table.shape[1] < 1 or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
-        raise ValueError("block_table must be [batch, max_pages] with contiguous rows")
-    b = block_table.shape[0]
-    if cache_seqlens.shape != (b,) or not cache_seqlens.is_contiguous():
-        raise ValueError("cache_seqlens must be a contiguous [batch] tensor")
-    if row_ptr.shape != (b + 1,) or not row_ptr.is_contiguous():
-        raise ValueError("row_ptr must be a contiguous [batch + 1] tensor")
-    if slots is None:
-        slots = torch.empty(tokens, dtype=torch.int64, device=block_table.device)
-    else:
-        _need(slots, "slots", index, torch.int64)
-        if slots.shape != (tokens,) or not slots.is_contiguous():
-            raise ValueError("slots must be a contiguous [tokens] tensor")
-    if positions is None:
-        positions = torch.empty(tokens, dtype=torch.int32, device=block_table.device)
-    else:
-        _need(positions, "positions", index, torch.int32)
-        if positions.shape != (tokens,) or not positions.is_contiguous():
-            raise ValueError("positions must be a contiguous [tokens] tensor")
-    _launch(index, load_library().mla_cache_slots, row_ptr.data_ptr(), cache_seqlens.data_ptr(), b,
-            block_table.data_ptr(), block_table.stride(0), block_table.shape[1], num_pages, tokens, slots.data_ptr(),
-            positions.data_ptr())
-    return slots, positions
-
-
-def _cache_write(entry: str, latent, rope, slots, pool, dtype_pool, scale, norm_weight, eps, positions, inv_freq,
-                 interleaved, magnitude) -> None:
-    index = _cuda_index(latent, "latent")
-    dtype = DTYPES.get(latent.dtype)
-    if dtype is None:
-        raise TypeError(f"latent must be bf16, fp16 or fp32 (got {latent.dtype})")
-    _need(rope, "rope", index, latent.dtype)
-    _need(slots, "slots", index, torch.int64)
-    _need(pool, "the cache", index, dtype_pool)
-    if latent.dim() != 3 or latent.shape[2] != D_V:
-        raise ValueError(f"latent must be [tokens, h_kv, {D_V}]")
-    T, h_kv, _ = latent.shape
-    if rope.shape != (T, h_kv, D_QK - D_V):
-        raise ValueError(f"rope must be [tokens, h_kv, {D_QK - D_V}]")
-    if latent.stride(2) != 1 or rope.stride(2) != 1:
-        raise ValueError("the last dimensions of latent and rope must be contiguous")
-    if slots.shape != (T,) or not slots.is_contiguous():
-        raise ValueError("slots must be a contiguous [tokens] tensor")
-    if pool.dim() != 4 or pool.shape[2] != h_kv or pool.shape[3] != D_QK or not pool.is_contiguous():
-        raise ValueError(f"the cache must be a contiguous [pages, {PAGE}, h_kv, {D_QK}] tensor")
-    weight = None
-    if norm_weight is not None:
-        _need(norm_weight, "norm_weight", index, latent.dtype)
-        if norm_weight.shape != (D_V,) or not norm_weight.is_contiguous():
-            raise ValueError(f"norm_weight must be a contiguous [{D_V}] tensor")
-        weight = norm_weight.data_ptr()
-    flags, pos, freq = 0, None, None
-    if inv_freq is not None:
-        if positions is None:
-            raise ValueError("inv_freq needs positions")
-        _need(inv_freq, "inv_freq", index, torch.float64)
-        if inv_freq.shape != ((D_QK - D_V) // 2,) or not inv_freq.is_contiguous():
-            raise ValueError(f"inv_freq must be a contiguous [{(D_QK - D_V) // 2}] tensor")
-        flags = _positions_flag(positions, T, index) | (0 if interleaved else MLA_ROPE_HALF)
-        pos, freq = positions.data_ptr(), inv_freq.data_ptr()
-    elif positions is not None:
-        raise ValueError("positions need inv_freq")
-    ls, rs = latent.stride(), rope.stride()
-    _launch(index, getattr(load_library(), entry), latent.data_ptr(), _I64x2(ls[0], ls[1]), rope.data_ptr(),
-            _I64x2(rs[0], rs[1]), dtype, T, h_kv, weight, eps, pos, freq, magnitude, flags, slots.data_ptr(),
-            pool.data_ptr(), *scale, pool.shape[0], pool.shape[1])
-
-
-def _codes(k8: torch.Tensor) -> torch.Tensor:
-    return k8.view(torch.uint8) if k8.dtype == torch.float8_e4m3fn else k8
-
-
-def _scale_ptr(k8: torch.Tensor, k_scale: torch.Tensor) -> int:
-    _need(k_scale, "k_scale", k8.get_device(), torch.float32)
-    if k8.dim() != 4 or k_scale.shape != (k8.shape[2], k8.shape[0], k8.shape[1]) or not k_scale.is_contiguous():
-        raise ValueError("k_scale must be a contiguous [h_kv, num_pages, page] tensor, k8 [num_pages, page, h_kv, d]")
-    return k_scale.data_ptr()
+    return (_binding or load_binding()).cache_slots(block_table, cache_seqlens, row_ptr, num_pages, tokens, slots, positions)
 
 
 def mla_cache_write(latent: torch.Tensor, rope: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
@@ -787,8 +635,8 @@ def mla_cache_write(latent: torch.Tensor, rope: torch.Tensor, slots: torch.Tenso
     and rope [T, h_kv, 64] are bf16, fp16 or fp32 with contiguous rows (views of one projection);
     the latent is RMS-normalised when ``norm_weight`` [512] is given, the rope columns are turned
     by ``positions`` [T] and ``inv_freq`` [32] when those are given (mla_rope)."""
-    _cache_write("mla_cache_write", latent, rope, slots, k_cache, torch.bfloat16, (), norm_weight, eps, positions,
-                 inv_freq, interleaved, magnitude)
+    (_binding or load_binding()).cache_write(latent, rope, slots, k_cache, None, norm_weight, eps, positions, inv_freq,
+                                             interleaved, magnitude)
 
 
 def mla_cache_write_fp8(latent: torch.Tensor, rope: torch.Tensor, slots: torch.Tensor, k8: torch.Tensor,
@@ -797,49 +645,20 @@ def mla_cache_write_fp8(latent: torch.Tensor, rope: torch.Tensor, slots: torch.T
                         interleaved: bool = True, magnitude: float = 1.0) -> None:
     """mla_cache_write into the FP8 cache of mla_decode_paged_fp8: k8 [pages, 64, h_kv, 576] E4M3
     codes (uint8 or float8_e4m3fn), k_scale [h_kv, pages, 64] fp32 = max|row| / 448."""
-    k8 = _codes(k8)
-    _cache_write("mla_cache_write_fp8", latent, rope, slots, k8, torch.uint8, (_scale_ptr(k8, k_scale),), norm_weight,
-                 eps, positions, inv_freq, interleaved, magnitude)
-
-
-def _cache_read(entry: str, pool, dtype_pool, scale, slots, out) -> torch.Tensor:
-    index = _cuda_index(pool, "the cache")
-    _need(pool, "the cache", index, dtype_pool)
-    _need(slots, "slots", index, torch.int64)
-    if pool.dim() != 4 or pool.shape[3] != D_QK or not pool.is_contiguous():
-        raise ValueError(f"the cache must be a contiguous [pages, {PAGE}, h_kv, {D_QK}] tensor")
-    if slots.dim() != 1 or not slots.is_contiguous():
-        raise ValueError("slots must be a contiguous 1-D tensor")
-    pages, page, h_kv, _ = pool.shape
-    T = slots.shape[0]
-    if out is None:
-        out = torch.empty((T, h_kv, D_QK), dtype=torch.bfloat16, device=pool.device)
-    else:
-        _need(out, "out", index, torch.bfloat16)
-        if out.shape != (T, h_kv, D_QK) or out.stride(2) != 1:
-            raise ValueError(f"out must be [tokens, h_kv, {D_QK}] with contiguous rows")
-        _require_rows_apart(out, "out")
-        if T:
-            (a, b), (c, d) = _extent(pool), _extent(out)
-            if a < d and c < b:
-                raise ValueError("out must not overlap the cache")
-    os = out.stride()
-    _launch(index, getattr(load_library(), entry), pool.data_ptr(), *scale, pages, page, h_kv, slots.data_ptr(), T,
-            out.data_ptr(), _I64x2(os[0], os[1]))
-    return out
+    (_binding or load_binding()).cache_write(latent, rope, slots, k8, k_scale, norm_weight, eps, positions, inv_freq,
+                                             interleaved, magnitude)
 
 
 def mla_cache_read(k_cache: torch.Tensor, slots: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rows of the cache by slot (int64 [T], mla_cache_slots): [T, h_kv, 576] bf16; a slot outside
     the pool gives a row of zeros.  ``out`` may be a view with contiguous rows."""
-    return _cache_read("mla_cache_read", k_cache, torch.bfloat16, (), slots, out)
+    return (_binding or load_binding()).cache_read(k_cache, None, slots, out)
 
 
 def mla_cache_read_fp8(k8: torch.Tensor, k_scale: torch.Tensor, slots: torch.Tensor,
                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """mla_cache_read of the FP8 cache: codes times their row's scale, rounded to bf16."""
-    k8 = _codes(k8)
-    return _cache_read("mla_cache_read_fp8", k8, torch.uint8, (_scale_ptr(k8, k_scale),), slots, out)
+    return (_binding or load_binding()).cache_read(k8, k_scale, slots, out)
 
 
 def mla_verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniform: torch.Tensor,
@@ -850,45 +669,7 @@ def mla_verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uni
     [0, 1), draft_probs [b, s, V] of the target's type (None: drafts chosen with certainty),
     num_drafts int32 [b] (None: s everywhere).  Returns (accepted int32 [b], tokens int32
     [b, s + 1]: the accepted drafts, the next token, then -1)."""
-    index = _cuda_index(target_probs, "target_probs")
-    dtype = DTYPES.get(target_probs.dtype)
-    if dtype is None:
-        raise TypeError(f"target_probs must be bf16, fp16 or fp32 (got {target_probs.dtype})")
-    _need(draft_tokens, "draft_tokens", index, torch.int32)
-    _need(uniform, "uniform", index, torch.float32)
-    _need(uniform_new, "uniform_new", index, torch.float32)
-    if target_probs.dim() != 3 or target_probs.shape[1] < 2 or target_probs.shape[2] < 1:
-        raise ValueError("target_probs must be [batch, drafts + 1, vocab] with at least one draft")
-    b, s1, V = target_probs.shape
-    s = s1 - 1
-    ts = target_probs.stride()
-    if ts[2] != 1 and V > 1:
-        raise ValueError("target_probs' last dimension must be contiguous")
-    if draft_tokens.shape != (b, s) or not draft_tokens.is_contiguous():
-        raise ValueError("draft_tokens must be a contiguous [batch, drafts] tensor")
-    if uniform.shape != (b, s) or not uniform.is_contiguous():
-        raise ValueError("uniform must be a contiguous [batch, drafts] tensor")
-    if uniform_new.shape != (b,) or not uniform_new.is_contiguous():
-        raise ValueError("uniform_new must be a contiguous [batch] tensor")
-    dptr = dst = nptr = None
-    if draft_probs is not None:
-        _need(draft_probs, "draft_probs", index, target_probs.dtype)
-        if draft_probs.shape != (b, s, V) or (draft_probs.stride(2) != 1 and V > 1):
-            raise ValueError("draft_probs must be [batch, drafts, vocab], its last dimension contiguous")
-        dptr, dst = draft_probs.data_ptr(), _I64x2(draft_probs.stride(0), draft_probs.stride(1))
-    if num_drafts is not None:
-        _need(num_drafts, "num_drafts", index, torch.int32)
-        if num_drafts.shape != (b,) or not num_drafts.is_contiguous():
-            raise ValueError("num_drafts must be a contiguous [batch] tensor")
-        nptr = num_drafts.data_ptr()
-    accepted = torch.empty(b, dtype=torch.int32, device=target_probs.device)
-    tokens = torch.empty((b, s1), dtype=torch.int32, device=target_probs.device)
-    if b == 0:
-        return accepted, tokens
-    _launch(index, load_library().mla_verify_draft, target_probs.data_ptr(), _I64x2(ts[0], ts[1]), dptr, dst, dtype,
-            draft_tokens.data_ptr(), uniform.data_ptr(), uniform_new.data_ptr(), nptr, b, s, V, accepted.data_ptr(),
-            tokens.data_ptr())
-    return accepted, tokens
+    return (_binding or load_binding()).verify_draft(target_probs, draft_tokens, uniform, uniform_new, draft_probs, num_drafts)
 
 
 def query_status(workspace: torch.Tensor) -> int:

@@ -1,0 +1,240 @@
+"""Host-side checks, without a GPU, of the operators around the decode: what the marshalling
+module and the C ABI refuse before anything reaches a device, and the frequency formulas."""
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+from paged_mla_decode_11_b200 import build as B
+from paged_mla_decode_11_b200 import ops
+
+bf, f32, i32, i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    B.build()
+    ops.load_binding()
+
+
+def z(*shape, dtype=bf):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def rope_args(**over):
+    a = dict(x=z(5, 4, 64), positions=z(5, dtype=i64), inv_freq=ops.rope_frequencies(64))
+    a.update(over)
+    return a
+
+
+@pytest.mark.parametrize("over,exc,msg", [
+    (dict(x=[1.0]), TypeError, "x must be a tensor"),
+    (dict(x=z(5, 4, 64, dtype=torch.float64)), TypeError, "x must be bf16"),
+    (dict(x=z(5, 64)), ValueError, "tokens, heads, width"),
+    (dict(x=z(5, 4, 128)[..., ::2]), ValueError, "last dimension"),
+    (dict(x=z(5, 4, 63)), ValueError, "inv_freq"),
+    (dict(inv_freq=ops.rope_frequencies(64).float()), TypeError, "inv_freq must be"),
+    (dict(inv_freq=torch.zeros(0, dtype=torch.float64)), ValueError, "inv_freq"),
+    (dict(inv_freq=torch.zeros(64, dtype=torch.float64)[::2]), ValueError, "inv_freq"),
+    (dict(positions=z(4, dtype=i64)), ValueError, "positions"),
+    (dict(positions=z(5, dtype=f32)), TypeError, "positions must be int32 or int64"),
+    (dict(positions=z(10, dtype=i64)[::2]), ValueError, "positions"),
+    (dict(out=z(5, 4, 32)), ValueError, "x's shape"),
+    (dict(out=z(5, 4, 64, dtype=f32)), TypeError, "out must be"),
+    (dict(out=z(1, 4, 64).expand(5, 4, 64)), ValueError, "rows of out"),
+    (dict(magnitude="m"), TypeError, "number"),
+    (dict(), ValueError, "CUDA tensor"),                       # all else is in order
+])
+def test_rope_refusals(over, exc, msg):
+    with pytest.raises(exc, match=msg):
+        ops.mla_rope(**rope_args(**over))
+
+
+def test_rope_refuses_partly_overlapping_rows():
+    base = z(5, 4, 200)
+    with pytest.raises(ValueError, match="must not overlap it"):
+        ops.mla_rope(**rope_args(x=base[..., :64], out=base[..., 8:72]))
+    with pytest.raises(ValueError, match="CUDA tensor"):       # in place passes the checks
+        x = base[..., 64:128]
+        ops.mla_rope(**rope_args(x=x, out=x))
+    with pytest.raises(ValueError, match="rows of out"):       # heads closer than their width
+        ops.mla_rope(**rope_args(out=torch.as_strided(z(5000), (5, 4, 64), (256, 32, 1))))
+    with pytest.raises(ValueError, match="CUDA tensor"):       # head-major rows are apart
+        ops.mla_rope(**rope_args(out=z(4, 5, 64).transpose(0, 1)))
+
+
+def write_args(fp8=False, **over):
+    both = z(6, 1, 576)
+    a = dict(latent=both[..., :512], rope=both[..., 512:], slots=z(6, dtype=i64))
+    a.update(dict(k8=z(3, 64, 1, 576, dtype=torch.uint8), k_scale=z(1, 3, 64, dtype=f32)) if fp8 else
+             dict(k_cache=z(3, 64, 1, 576)))
+    a.update(over)
+    return a
+
+
+@pytest.mark.parametrize("over,exc,msg", [
+    (dict(latent=z(6, 1, 512, dtype=torch.int8)), TypeError, "latent must be"),
+    (dict(rope=z(6, 1, 64, dtype=f32)), TypeError, "rope must be"),
+    (dict(latent=z(6, 512)), ValueError, "latent must be"),
+    (dict(latent=z(6, 1, 576)), ValueError, "latent must be"),
+    (dict(rope=z(6, 1, 32)), ValueError, "rope must be"),
+    (dict(rope=z(5, 1, 64)), ValueError, "rope must be"),
+    (dict(latent=z(6, 1, 1024)[..., ::2]), ValueError, "last dimensions"),
+    (dict(slots=z(6, dtype=i32)), TypeError, "slots must be"),
+    (dict(slots=z(7, dtype=i64)), ValueError, "slots must be"),
+    (dict(norm_weight=z(512, dtype=f32)), TypeError, "norm_weight"),
+    (dict(norm_weight=z(576)), ValueError, "norm_weight"),
+    (dict(positions=z(6, dtype=i32)), ValueError, "positions need inv_freq"),
+    (dict(inv_freq=ops.rope_frequencies(64)), ValueError, "inv_freq needs positions"),
+    (dict(positions=z(6, dtype=i32), inv_freq=ops.rope_frequencies(32)), ValueError, "inv_freq"),
+    (dict(positions=z(5, dtype=i32), inv_freq=ops.rope_frequencies(64)), ValueError, "positions"),
+    (dict(), ValueError, "CUDA tensor"),
+])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_write_refusals(over, exc, msg, fp8):
+    with pytest.raises(exc, match=msg):
+        (ops.mla_cache_write_fp8 if fp8 else ops.mla_cache_write)(**write_args(fp8, **over))
+
+
+@pytest.mark.parametrize("call,over,exc,msg", [
+    ("write", dict(k_cache=z(3, 64, 1, 576, dtype=f32)), TypeError, "k_cache must be bf16"),
+    ("write", dict(k_cache=z(3, 64, 2, 576)), ValueError, "h_kv"),
+    ("write", dict(k_cache=z(3, 32, 1, 576)), ValueError, "the cache must be"),
+    ("write", dict(k_cache=z(3, 64, 1, 600)[..., :576]), ValueError, "the cache must be"),
+    ("write8", dict(k8=z(3, 64, 1, 576)), TypeError, "k8 must be"),
+    ("write8", dict(k_scale=z(3, 64, 1, dtype=f32)), ValueError, "k_scale"),
+    ("write8", dict(k_scale=z(1, 3, 64)), TypeError, "k_scale"),
+    ("read", dict(k_cache=z(3, 64, 1, 576, dtype=torch.uint8)), TypeError, "k_cache must be bf16"),
+    ("read", dict(slots=z(2, 2, dtype=i64)), ValueError, "slots must be"),
+    ("read", dict(slots=z(2, dtype=i32)), TypeError, "slots must be"),
+    ("read", dict(out=z(6, 1, 512)), ValueError, "out must be"),
+    ("read", dict(out=z(6, 1, 576, dtype=f32)), TypeError, "out must be"),
+    ("read", dict(out=z(1, 1, 576).expand(6, 1, 576)), ValueError, "rows of out"),
+    ("read", dict(), ValueError, "CUDA tensor"),
+    ("read8", dict(k_scale=z(2, 3, 64, dtype=f32)), ValueError, "k_scale"),
+    ("read8", dict(), ValueError, "CUDA tensor"),
+])
+def test_pool_refusals(call, over, exc, msg):
+    a = write_args(call.endswith("8"), **over)
+    if call.startswith("read"):
+        a = {k: v for k, v in a.items() if k not in ("latent", "rope")}
+    fn = dict(write=ops.mla_cache_write, write8=ops.mla_cache_write_fp8, read=ops.mla_cache_read, read8=ops.mla_cache_read_fp8)[call]
+    with pytest.raises(exc, match=msg):
+        fn(**a)
+
+
+def test_read_refuses_an_output_inside_the_cache():
+    pool = z(3, 64, 1, 576)
+    with pytest.raises(ValueError, match="overlap the cache"):
+        ops.mla_cache_read(pool, z(6, dtype=i64), out=pool.view(-1, 1, 576)[10:16])
+
+
+@pytest.mark.parametrize("over,exc,msg", [
+    (dict(block_table=z(3, 4, dtype=i64)), TypeError, "block_table"),
+    (dict(block_table=z(4, 3, dtype=i32).t()), ValueError, "block_table"),
+    (dict(cache_seqlens=z(2, dtype=i32)), ValueError, "cache_seqlens"),
+    (dict(row_ptr=z(3, dtype=i32)), ValueError, "row_ptr"),
+    (dict(tokens=-1), ValueError, "tokens"),
+    (dict(slots=z(9, dtype=i64)), ValueError, "slots"),
+    (dict(positions=z(10, dtype=i64)), TypeError, "positions"),
+    (dict(), ValueError, "CUDA tensor"),
+])
+def test_slot_refusals(over, exc, msg):
+    a = dict(block_table=z(3, 4, dtype=i32), cache_seqlens=z(3, dtype=i32), row_ptr=z(4, dtype=i32), num_pages=12, tokens=10)
+    a.update(over)
+    with pytest.raises(exc, match=msg):
+        ops.mla_cache_slots(**a)
+
+
+@pytest.mark.parametrize("over,exc,msg", [
+    (dict(target_probs=z(2, 4, 9, dtype=torch.int32)), TypeError, "target_probs"),
+    (dict(target_probs=z(2, 1, 9, dtype=f32)), ValueError, "at least one draft"),
+    (dict(target_probs=z(2, 4, 18, dtype=f32)[..., ::2]), ValueError, "last dimension"),
+    (dict(draft_tokens=z(2, 3, dtype=i64)), TypeError, "draft_tokens"),
+    (dict(draft_tokens=z(2, 4, dtype=i32)), ValueError, "draft_tokens"),
+    (dict(uniform=z(3, 2, dtype=f32).t()), ValueError, "uniform"),
+    (dict(uniform_new=z(3, dtype=f32)), ValueError, "uniform_new"),
+    (dict(draft_probs=z(2, 3, 9)), TypeError, "draft_probs"),
+    (dict(draft_probs=z(2, 4, 9, dtype=f32)), ValueError, "draft_probs"),
+    (dict(num_drafts=z(2, dtype=i64)), TypeError, "num_drafts"),
+    (dict(num_drafts=z(1, dtype=i32)), ValueError, "num_drafts"),
+    (dict(), ValueError, "CUDA tensor"),
+])
+def test_verify_refusals(over, exc, msg):
+    a = dict(target_probs=z(2, 4, 9, dtype=f32), draft_tokens=z(2, 3, dtype=i32), uniform=z(2, 3, dtype=f32),
+             uniform_new=z(2, dtype=f32))
+    a.update(over)
+    with pytest.raises(exc, match=msg):
+        ops.mla_verify_draft(**a)
+
+
+def test_c_abi_refusals():
+    """Every refusal below comes before any device call; the addresses are never read."""
+    lib = ops.load_library()
+    s2 = (ctypes.c_int64 * 2)(576, 576)
+    odd = (ctypes.c_int64 * 2)(577, 576)
+    neg = (ctypes.c_int64 * 2)(-576, 576)
+    err = lib.mla_last_error_string
+
+    def rope(x=16, xs=s2, dtype=0, T=4, H=2, D=64, n=32, pos=16, f=16, m=1.0, flags=0, out=32, os=s2):
+        return lib.mla_rope(x, xs, dtype, T, H, D, n, pos, f, m, flags, out, os, None)
+    assert rope(dtype=3) == -1 and b"element type" in err()
+    assert rope(n=0) == -1 and rope(n=33) == -1 and rope(D=70000, n=2) == -1
+    assert rope(flags=8) == -1 and b"flags" in err()
+    assert rope(m=math.inf) == -1 and b"magnitude" in err()
+    assert rope(x=None) == -1 and rope(pos=None) == -1 and rope(f=None) == -1
+    assert rope(T=-1) == -1 and rope(H=0) == -1 and rope(H=65536) == -1
+    assert rope(xs=neg) == -1 and rope(os=neg) == -1
+    assert rope(x=17) == -1 and rope(dtype=2, x=18) == -1 and rope(pos=20, flags=4) == -1 and b"aligned" in err()
+    assert rope(x=32, out=32, os=odd) == -1 and b"strides of x" in err()
+    assert rope(T=0, x=None, out=None) == 0                        # nothing to do
+
+    def slots(ptr=16, lens=16, b=2, table=16, bs=4, w=4, pages=8, T=4, s=16, p=16):
+        return lib.mla_cache_slots(ptr, lens, b, table, bs, w, pages, T, s, p, None)
+    assert slots(b=0) == -1 and slots(T=-1) == -1 and slots(w=0) == -1 and slots(bs=-1) == -1 and slots(pages=0) == -1
+    assert slots(ptr=None) == -1 and slots(s=None) == -1 and slots(s=20) == -1
+    assert slots(T=0, s=None) == 0
+
+    def write(lat=16, ls=s2, rp=16, rs=s2, dtype=0, T=4, h=1, w=None, eps=1e-6, pos=None, f=None, m=1.0, flags=0, at=16,
+              pool=16, pages=8, page=64):
+        return lib.mla_cache_write(lat, ls, rp, rs, dtype, T, h, w, eps, pos, f, m, flags, at, pool, pages, page, None)
+    assert write(page=32) == -2 and b"page_size" in err()
+    assert write(dtype=-1) == -1 and write(flags=2) == -1 and write(h=0) == -1 and write(pages=0) == -1
+    assert write(w=16, eps=-1.0) == -1 and b"eps" in err()
+    assert write(f=16) == -1 and b"null" in err()                  # frequencies without positions
+    assert write(ls=odd) == -1 and write(rs=neg) == -1 and b"multiples of 8" in err()
+    assert write(lat=24) == -1 and write(w=24) == -1 and write(at=20) == -1 and b"aligned" in err()
+    assert write(T=1 << 32) == -1 and b"2^31" in err()
+    assert write(T=0, lat=None) == 0
+    assert lib.mla_cache_write_fp8(16, s2, 16, s2, 0, 4, 1, None, 1e-6, None, None, 1.0, 0, 16, 16, None, 8, 64, None) == -1
+
+    def read(pool=16, pages=8, page=64, h=1, at=16, T=4, out=16, os=s2):
+        return lib.mla_cache_read(pool, pages, page, h, at, T, out, os, None)
+    assert read(page=128) == -2 and read(pages=0) == -1 and read(pool=None) == -1 and read(out=24) == -1 and read(os=odd) == -1
+    assert read(T=0, out=None) == 0
+    assert lib.mla_cache_read_fp8(16, None, 8, 64, 1, 16, 4, 16, s2, None) == -1
+
+    def verify(t=16, ts=s2, d=16, ds=s2, dtype=0, tok=16, u=16, un=16, n=None, b=2, s=3, V=9, acc=16, out=16):
+        return lib.mla_verify_draft(t, ts, d, ds, dtype, tok, u, un, n, b, s, V, acc, out, None)
+    assert verify(t=None) == -1 and verify(d=16, ds=None) == -1 and verify(un=None) == -1
+    assert verify(b=0) == -1 and verify(s=0) == -1 and verify(V=0) == -1 and verify(dtype=7) == -1
+    assert verify(ts=neg) == -1 and verify(ds=neg) == -1 and verify(tok=18) == -1 and b"aligned" in err()
+
+    # the FP8 decode of any number of rows checks what the 16-row one checks, but for the rows
+    s3 = (ctypes.c_int64 * 3)(576, 576, 576)
+
+    def rows(h_q=128, d=576, dv=512, page=64, flags=0, k8=16, scale=0.04):
+        return lib.mla_decode_paged_fp8_rows(16, s3, 1, 1, h_q, d, k8, 16, 1, page, 1, 16, 1, 16, dv, 16, 1, 16,
+                                             ctypes.c_float(scale), 1, 16, 16, 256, 1 << 20, flags, None)
+    assert rows(d=512) == -2 and rows(dv=256) == -2 and rows(page=32) == -2
+    assert rows(flags=2) == -1 and rows(k8=None) == -1 and rows(scale=-1.0) == -1 and rows(k8=24) == -1
+
+
+def test_frequency_refusals():
+    for bad in (dict(dim=63), dict(dim=0), dict(base=1.0), dict(factor=0.5), dict(scaling="cubic"),
+                dict(scaling="yarn", factor=4.0, beta_fast=1.0, beta_slow=2.0), dict(dim=2, scaling="ntk", factor=2.0)):
+        with pytest.raises(ValueError):
+            ops.rope_frequencies(**bad)
+    assert ops.rope_magnitude(1.0) == 1.0 and math.isclose(ops.rope_magnitude(40.0), 0.1 * math.log(40.0) + 1)
