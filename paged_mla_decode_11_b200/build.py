@@ -77,7 +77,7 @@ def _build_binding(verbose: bool) -> None:
     cmd += [src, "-o", tmp, "-ldl"]
     for d in cpp_extension.library_paths():
         cmd += ["-L", d]
-    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)

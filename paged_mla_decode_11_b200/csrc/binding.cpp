@@ -6,11 +6,13 @@
 #include <dlfcn.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <string>
 
 #include "pagedmla.h"
@@ -25,6 +27,7 @@ struct Api {
   decltype(&mla_cache_read) cache_read;
   decltype(&mla_cache_read_fp8) cache_read_fp8;
   decltype(&mla_verify_draft) verify_draft;
+  decltype(&mla_decode_paged_fp8_rows) decode_fp8_rows;
   decltype(&mla_last_error_string) last_error;
 } api;
 PyObject *mla_error = nullptr;  // ops.MlaError
@@ -96,6 +99,9 @@ struct Place {
   c10::Device device;
   Place(const at::Tensor &t, const char *name) : device(t.device()) {
     if (!device.is_cuda()) refuse_value(std::string(name) + " must be a CUDA tensor");
+  }
+  at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type) const {
+    return at::detail::empty_cuda(sizes, type, device, std::nullopt);
   }
   void same(const at::Tensor &t, const char *name) const {
     if (t.device() != device)
@@ -180,7 +186,7 @@ PyObject *rope(PyObject *const *a, Py_ssize_t n) {
   if (given(a[6]))
     place.same(*out, "out");
   else
-    fresh = at::empty({T, H, D}, x.options());
+    fresh = place.empty({T, H, D}, x.scalar_type());
   if (out->numel() > 0) {
     const int64_t xs[2] = {x.stride(0), x.stride(1)}, os[2] = {out->stride(0), out->stride(1)};
     launch(place, [&](mla_stream_t stream) {
@@ -223,7 +229,7 @@ PyObject *cache_slots(PyObject *const *a, Py_ssize_t n) {
     if (given(a[5 + i]))
       place.same(*out[i], names[i]);
     else
-      fresh[i] = at::empty({tokens}, table.options().dtype(types[i]));
+      fresh[i] = place.empty({tokens}, types[i]);
   launch(place, [&](mla_stream_t stream) {
     return api.cache_slots(static_cast<const int32_t *>(ptr.const_data_ptr()), static_cast<const int32_t *>(lens.const_data_ptr()),
                            int(b), static_cast<const int32_t *>(table.const_data_ptr()), table.stride(0), int(table.size(1)),
@@ -333,7 +339,7 @@ PyObject *cache_read(PyObject *const *a, Py_ssize_t n) {
   if (given(a[3]))
     place.same(*out, "out");
   else
-    fresh = at::empty({T, h_kv, kRow}, pool.options().dtype(at::kBFloat16));
+    fresh = place.empty({T, h_kv, kRow}, at::kBFloat16);
   if (out->numel() > 0) {
     const int64_t os[2] = {out->stride(0), out->stride(1)};
     const int64_t *at = static_cast<const int64_t *>(slots.const_data_ptr());
@@ -383,7 +389,7 @@ PyObject *verify_draft(PyObject *const *a, Py_ssize_t n) {
   place.same(uniform_new, "uniform_new");
   if (draft) place.same(*draft, "draft_probs");
   if (num) place.same(*num, "num_drafts");
-  at::Tensor accepted = at::empty({b}, tokens.options()), made = at::empty({b, s + 1}, tokens.options());
+  at::Tensor accepted = place.empty({b}, at::kInt), made = place.empty({b, s + 1}, at::kInt);
   if (b > 0) {
     const int64_t ts[2] = {target.stride(0), target.stride(1)};
     const int64_t ds[2] = {draft ? draft->stride(0) : 0, draft ? draft->stride(1) : 0};
@@ -397,6 +403,75 @@ PyObject *verify_draft(PyObject *const *a, Py_ssize_t n) {
     });
   }
   PyObject *first = THPVariable_Wrap(std::move(accepted)), *second = THPVariable_Wrap(std::move(made));
+  return Py_BuildValue("(NN)", first, second);
+}
+
+// decode_fp8_rows(q, k8, k_scale, block_table, cache_seqlens, dv, tile_metadata, num_splits, softmax_scale,
+//                 causal, workspace, out, lse, skip_combine)
+PyObject *decode_fp8_rows(PyObject *const *a, Py_ssize_t n) {
+  need_arguments(n, 14);
+  const at::Tensor &q = tensor(a[0], "q"), &k8 = tensor(a[1], "k8"), &scale = tensor(a[2], "k_scale"),
+                   &table = tensor(a[3], "block_table"), &lens = tensor(a[4], "cache_seqlens"),
+                   &tile = tensor(a[6], "tile_metadata"), &splits = tensor(a[7], "num_splits");
+  need_type(q, "q", at::kBFloat16);
+  need_type(table, "block_table", at::kInt);
+  need_type(lens, "cache_seqlens", at::kInt);
+  need_type(tile, "tile_metadata", at::kInt);
+  need_type(splits, "num_splits", at::kInt);
+  if (q.dim() != 4 || table.dim() != 2) refuse_value("q must be 4-D, block_table 2-D");
+  need_pool(k8, &scale);
+  const int64_t b = q.size(0), s_q = q.size(1), h_q = q.size(2), d = q.size(3), dv = to_int(a[5]), h_kv = k8.size(2);
+  if (d != kRow) refuse_value("q and k8 disagree on the latent width");
+  if (q.stride(3) != 1) refuse_value("q's last dimension must be contiguous");
+  if (table.size(0) != b || !rows_contiguous(table)) refuse_value("block_table must be [batch, max_pages] with contiguous rows");
+  need_vector(lens, "cache_seqlens", "batch", b);
+  if (tile.dim() != 2 || tile.size(1) != MLA_TILE_FIELDS || !tile.is_contiguous())
+    refuse_value("tile_metadata must be a contiguous [num_parts, 8] tensor");
+  need_vector(splits, "num_splits", "batch + 1", b + 1);
+  if (b > INT32_MAX || s_q > INT32_MAX || h_q > INT32_MAX || h_kv > INT32_MAX || tile.size(0) > INT32_MAX || dv < 0 || dv > 4096)
+    refuse_value("a dimension is out of range");
+  const float softmax_scale = given(a[8]) ? to_float(a[8]) : 1.f / std::sqrt(float(d));
+  const bool causal = truth(a[9]);
+  at::Tensor fresh_out, fresh_lse;
+  const at::Tensor *out = &fresh_out, *lse = &fresh_lse;
+  if (given(a[11])) {
+    out = &tensor(a[11], "out");
+    if (out->sizes() != at::IntArrayRef({b, s_q, h_q, dv}) || out->scalar_type() != at::kBFloat16 || !out->is_contiguous())
+      refuse_value("out must be a contiguous bf16 [b, s_q, h_q, dv] tensor");
+  }
+  if (given(a[12])) {
+    lse = &tensor(a[12], "lse");
+    if (lse->sizes() != at::IntArrayRef({b, h_q, s_q}) || lse->scalar_type() != at::kFloat || !lse->is_contiguous())
+      refuse_value("lse must be a contiguous fp32 [b, h_q, s_q] tensor");
+  }
+  const Place place(q, "q");
+  place.same(k8, "k8");
+  place.same(scale, "k_scale");
+  place.same(table, "block_table");
+  place.same(lens, "cache_seqlens");
+  place.same(tile, "tile_metadata");
+  place.same(splits, "num_splits");
+  const at::Tensor &workspace = tensor(a[10], "workspace");
+  need_type(workspace, "workspace", at::kByte);
+  if (!workspace.is_contiguous()) refuse_value("workspace must be contiguous");
+  place.same(workspace, "workspace");
+  if (given(a[11])) place.same(*out, "out");
+  if (given(a[12])) place.same(*lse, "lse");
+  if (!given(a[11])) fresh_out = place.empty({b, s_q, h_q, dv}, at::kBFloat16);
+  if (!given(a[12])) fresh_lse = place.empty({b, h_q, s_q}, at::kFloat);
+  const int64_t qs[3] = {q.stride(0), q.stride(1), q.stride(2)};
+  const unsigned flags = truth(a[13]) ? MLA_FLAG_SKIP_COMBINE : 0;
+  launch(place, [&](mla_stream_t stream) {
+    return api.decode_fp8_rows(
+        q.const_data_ptr(), qs, int(b), int(s_q), int(h_q), int(d), k8.const_data_ptr(),
+        static_cast<const float *>(scale.const_data_ptr()), k8.size(0), int(k8.size(1)), int(h_kv),
+        static_cast<const int32_t *>(table.const_data_ptr()), table.stride(0),
+        static_cast<const int32_t *>(lens.const_data_ptr()), int(dv), static_cast<const int32_t *>(tile.const_data_ptr()),
+        int(tile.size(0)), static_cast<const int32_t *>(splits.const_data_ptr()), softmax_scale, causal, out->data_ptr(),
+        static_cast<float *>(lse->data_ptr()), workspace.data_ptr(), size_t(workspace.numel()), flags, stream);
+  });
+  PyObject *first = given(a[11]) ? Py_NewRef(a[11]) : THPVariable_Wrap(std::move(fresh_out));
+  PyObject *second = given(a[12]) ? Py_NewRef(a[12]) : THPVariable_Wrap(std::move(fresh_lse));
   return Py_BuildValue("(NN)", first, second);
 }
 
@@ -417,6 +492,7 @@ PyObject *bind(PyObject *const *a, Py_ssize_t n) {
   find(found.cache_read, "mla_cache_read");
   find(found.cache_read_fp8, "mla_cache_read_fp8");
   find(found.verify_draft, "mla_verify_draft");
+  find(found.decode_fp8_rows, "mla_decode_paged_fp8_rows");
   find(found.last_error, "mla_last_error_string");
   api = found;
   Py_INCREF(a[1]);
@@ -448,6 +524,7 @@ PyMethodDef methods[] = {method<bind>("bind"),
                          method<cache_write>("cache_write"),
                          method<cache_read>("cache_read"),
                          method<verify_draft>("verify_draft"),
+                         method<decode_fp8_rows>("decode_fp8_rows"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};
 

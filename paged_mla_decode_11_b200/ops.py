@@ -342,24 +342,6 @@ def mla_decode_paged_fp8(q: torch.Tensor, k8: torch.Tensor, k_scale: torch.Tenso
     """Paged MLA decode over an FP8 latent cache: k8 [pages, 64, h_kv, 576] uint8 E4M3 codes
     (or float8_e4m3fn), k_scale [h_kv, pages, 64] fp32, one scale per token and latent head;
     up to 16 query rows per latent head.  Other arguments and results as mla_decode_paged."""
-    return _decode_fp8("mla_decode_paged_fp8", q, k8, k_scale, block_table, cache_seqlens, dv, tile_metadata,
-                       num_splits, softmax_scale, causal, workspace, out, lse, skip_combine)
-
-
-def mla_decode_paged_fp8_rows(q: torch.Tensor, k8: torch.Tensor, k_scale: torch.Tensor, block_table: torch.Tensor,
-                              cache_seqlens: torch.Tensor, dv: int, tile_metadata: torch.Tensor,
-                              num_splits: torch.Tensor, softmax_scale: Optional[float] = None,
-                              causal: bool = False, workspace: Optional[torch.Tensor] = None,
-                              out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                              skip_combine: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
-    """mla_decode_paged_fp8 for any number of query rows per latent head (above 16 a CTA-pair
-    tensor-core kernel on the codes themselves)."""
-    return _decode_fp8("mla_decode_paged_fp8_rows", q, k8, k_scale, block_table, cache_seqlens, dv, tile_metadata,
-                       num_splits, softmax_scale, causal, workspace, out, lse, skip_combine)
-
-
-def _decode_fp8(entry, q, k8, k_scale, block_table, cache_seqlens, dv, tile_metadata, num_splits, softmax_scale, causal,
-                workspace, out, lse, skip_combine) -> Tuple[torch.Tensor, torch.Tensor]:
     _require_cuda(q, "q", torch.bfloat16)
     if k8.dtype == torch.float8_e4m3fn:
         k8 = k8.view(torch.uint8)
@@ -404,13 +386,29 @@ def _decode_fp8(entry, q, k8, k_scale, block_table, cache_seqlens, dv, tile_meta
     if workspace is None:
         workspace = _default_workspace(workspace_size(b, s_q, h_q, h_kv, num_parts), dev)
     qst = q.stride()
-    _check(getattr(load_library(), entry)(
+    _check(load_library().mla_decode_paged_fp8(
         q.data_ptr(), _I64x3(qst[0], qst[1], qst[2]), b, s_q, h_q, d, k8.data_ptr(), k_scale.data_ptr(),
         num_pages, page, h_kv, block_table.data_ptr(), block_table.stride(0), cache_seqlens.data_ptr(), dv,
         tile_metadata.data_ptr(), num_parts, num_splits.data_ptr(), scale, int(bool(causal)), out.data_ptr(),
         lse.data_ptr(), workspace.data_ptr(), workspace.numel(), MLA_FLAG_SKIP_COMBINE if skip_combine else 0,
         _stream_ptr(dev)))
     return out, lse
+
+
+def mla_decode_paged_fp8_rows(q: torch.Tensor, k8: torch.Tensor, k_scale: torch.Tensor, block_table: torch.Tensor,
+                              cache_seqlens: torch.Tensor, dv: int, tile_metadata: torch.Tensor,
+                              num_splits: torch.Tensor, softmax_scale: Optional[float] = None,
+                              causal: bool = False, workspace: Optional[torch.Tensor] = None,
+                              out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                              skip_combine: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """mla_decode_paged_fp8 for any number of query rows per latent head (above 16 a CTA-pair
+    tensor-core kernel on the codes themselves)."""
+    if workspace is None and q.dim() == 4 and k8.dim() == 4 and tile_metadata.dim() == 2 and q.is_cuda:
+        b, s_q, h_q, _ = q.shape
+        workspace = _default_workspace(workspace_size(b, s_q, h_q, k8.shape[2], tile_metadata.shape[0]), q.device)
+    return (_binding or load_binding()).decode_fp8_rows(q, k8, k_scale, block_table, cache_seqlens, dv, tile_metadata,
+                                                        num_splits, softmax_scale, causal, workspace, out, lse,
+                                                        skip_combine)
 
 
 def mla_combine(num_splits: torch.Tensor, s_q: int, h_q: int, h_kv: int, num_parts: int,

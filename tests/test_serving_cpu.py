@@ -170,6 +170,35 @@ def test_verify_refusals(over, exc, msg):
         ops.mla_verify_draft(**a)
 
 
+@pytest.mark.parametrize("over,exc,msg", [
+    (dict(q=z(3, 1, 128, 576, dtype=f32)), TypeError, "q must be"),
+    (dict(q=z(3, 128, 576)), ValueError, "4-D"),
+    (dict(q=z(3, 1, 128, 512)), ValueError, "latent width"),
+    (dict(q=z(3, 1, 128, 1152)[..., ::2]), ValueError, "last dimension"),
+    (dict(k8=z(10, 64, 1, 576)), TypeError, "k8 must be"),
+    (dict(k8=z(10, 64, 1, 600, dtype=torch.uint8)[..., :576]), ValueError, "the cache must be"),
+    (dict(k_scale=z(1, 9, 64, dtype=f32)), ValueError, "k_scale"),
+    (dict(block_table=z(2, 6, dtype=i32)), ValueError, "block_table"),
+    (dict(block_table=z(6, 3, dtype=i32).t()), ValueError, "block_table"),
+    (dict(cache_seqlens=z(4, dtype=i32)), ValueError, "cache_seqlens"),
+    (dict(tile_metadata=z(5, 7, dtype=i32)), ValueError, "tile_metadata"),
+    (dict(num_splits=z(3, dtype=i32)), ValueError, "num_splits"),
+    (dict(num_splits=z(4, dtype=i64)), TypeError, "num_splits"),
+    (dict(out=z(3, 1, 128, 256)), ValueError, "out must be"),
+    (dict(lse=z(3, 1, 128, dtype=f32)), ValueError, "lse must be"),
+    (dict(dv=-1), ValueError, "out of range"),
+    (dict(softmax_scale="s"), TypeError, "number"),
+    (dict(), ValueError, "CUDA tensor"),
+])
+def test_decode_rows_refusals(over, exc, msg):
+    a = dict(q=z(3, 1, 128, 576), k8=z(10, 64, 1, 576, dtype=torch.uint8), k_scale=z(1, 10, 64, dtype=f32),
+             block_table=z(3, 6, dtype=i32), cache_seqlens=z(3, dtype=i32), dv=512, tile_metadata=z(5, 8, dtype=i32),
+             num_splits=z(4, dtype=i32))
+    a.update(over)
+    with pytest.raises(exc, match=msg):
+        ops.mla_decode_paged_fp8_rows(**a)
+
+
 def test_c_abi_refusals():
     """Every refusal below comes before any device call; the addresses are never read."""
     lib = ops.load_library()
