@@ -233,7 +233,8 @@ MLA_API int mla_decode_paged_fp8(const void *q, const int64_t q_strides[3], int 
  * the key scales are each carried as a sum of two 8-bit terms.  The query's sum is exact for
  * values down to 2^-10 of the row's largest and within 2^-18 of the largest below; the
  * probabilities' is within 2^-8 of the value (as a bf16 rounding) or 2^-20 of the row's largest.
- * k_scale must be finite for every key; a query row that holds an infinity or NaN gives NaN in
+ * k_scale must be finite for every key (a block-table entry outside the pool reads some page of
+ * it); a query row that holds an infinity or NaN gives NaN in
  * its own rows only.  Scales below 2^-100 lose precision.  All arguments, layouts, results and
  * other errors as in mla_decode_paged_fp8.
  */
@@ -369,7 +370,7 @@ MLA_API int mla_absorb_output(const void *o_latent, const int64_t latent_strides
  *              that does not overlap x.  Rows of out must not overlap each other
  * Rotated in fp32, rounded once.  Rows whose sizes, strides and addresses are multiples of 16
  * bytes are moved 16 bytes at a time, others an element at a time.  tokens = 0 enqueues
- * nothing.  tokens <= 2^31, heads <= 65535, pairs in [1, 512], width <= 65536.
+ * nothing.  tokens < 2^31, heads <= 65535, pairs in [1, 512], width <= 65536.
  * A programmatic dependent launch that waits for the kernel before it.
  * Errors: MLA_ERR_ARG, MLA_ERR_CUDA.
  */

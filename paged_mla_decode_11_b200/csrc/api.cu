@@ -771,7 +771,7 @@ int mla_rope(const void *x, const int64_t x_strides[2], int dtype, int64_t token
   if (tokens == 0) return MLA_OK;
   if (!x || !x_strides || !positions || !inv_freq || !out || !out_strides)
     return fail(MLA_ERR_ARG, "null pointer argument");
-  if (tokens > (int64_t(1) << 31) || heads > 65535) return fail(MLA_ERR_ARG, "too many tokens or heads");
+  if (tokens >= (int64_t(1) << 31) || heads > 65535) return fail(MLA_ERR_ARG, "too many tokens or heads");
   for (int i = 0; i < 2; ++i)
     if (x_strides[i] < 0 || out_strides[i] < 0) return fail(MLA_ERR_ARG, "strides must be non-negative");
   const size_t size = dtype == MLA_DTYPE_F32 ? 4 : 2;

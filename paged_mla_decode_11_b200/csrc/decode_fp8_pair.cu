@@ -294,11 +294,12 @@ struct Groups {
     }
     if (++j == ngroups) seek(p, pc, prow0, seq + 1);
   }
-  // The group's two pages; a lone last page stands for both (its second half is masked).
-  __device__ __forceinline__ void pages(const DecodeParams &p, int &a, int &b) const {
+  // The group's two pages; a lone last page stands for both (its second half is masked).  Numbers
+  // outside the pool are moved into it: TMA would fill their pages, but scales are plain copies.
+  __device__ __forceinline__ void pages(const DecodeParams &p, int num_pages, int &a, int &b) const {
     const int32_t *row = p.block_table + int64_t(seq) * p.bt_stride + t0 / kPage;
-    a = row[2 * j];
-    b = row[min(2 * j + 1, ntiles - 1)];
+    a = min(max(row[2 * j], 0), num_pages - 1);
+    b = min(max(row[min(2 * j + 1, ntiles - 1)], 0), num_pages - 1);
   }
 };
 
@@ -308,7 +309,7 @@ struct Groups {
 // latent heads).
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
     decode_fp8_pair_kernel(const __grid_constant__ CUtensorMap k8_map, const __grid_constant__ CUtensorMap page_map,
-                           const __grid_constant__ CUtensorMap half_map, const DecodeParams p, const float *__restrict__ k_scale, int64_t scale_head) {
+                           const __grid_constant__ CUtensorMap half_map, const DecodeParams p, const float *__restrict__ k_scale, int num_pages) {
   using T = FpPair;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -373,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
     }
     // pages are read by both CTAs of the pair (the second time from L2)
     const uint64_t policy = l2_evict_normal_policy();
-    const float *scales = k_scale + int64_t(kvh) * scale_head;
+    const float *scales = k_scale + int64_t(kvh) * num_pages * kPage;
     Groups wa, wb;  // own pages, partner value halves
     wa.start(p, pc, prow0);
     wb = wa;
@@ -385,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
       // the partner page's value half of a group, once its score is done
       if (wb.count < wa.count && all_lanes(mbar_test_wait(bar(T::SFULL + wb.stage), wb.phase))) {
         int pa, pb;
-        wb.pages(p, pa, pb);
+        wb.pages(p, num_pages, pa, pb);
         if (lane == 0) {
           if (leader) mbar_arrive_expect_tx(bar(T::VFULL + wb.stage), 2 * T::kHalfVBytes);
           load_blocks_for_pair(slot(wb.stage, leader ? 2 : 0), &half_map, bar_cta0(T::VFULL + wb.stage),
@@ -399,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
       if (!progressed && !wa.done &&
           (wa.count < T::kStages || all_lanes(mbar_test_wait(bar(T::EMPTY + wa.stage), wa.phase ^ 1)))) {
         int pa, pb;
-        wa.pages(p, pa, pb);
+        wa.pages(p, num_pages, pa, pb);
         const int phys = leader ? pa : pb, st = wa.stage;
         if (lane == 0) {
           if (leader) mbar_arrive_expect_tx(bar(T::FULL + st), 2 * T::kOwnBytes);
@@ -878,7 +879,7 @@ cudaError_t launch_decode_fp8_pair(const CUtensorMap &k8_map, const CUtensorMap 
   if (e != cudaSuccess) return e;
   const unsigned pairs = unsigned((p.R + 2 * T::BM - 1) / (2 * T::BM));
   return launch_early(decode_fp8_pair_kernel, dim3(2 * pairs, p.num_parts, p.h_kv), dim3(T::kThreads), T::kSmemBytes,
-                      stream, k8_map, page_map, half_map, p, k_scale, num_pages * kPage);
+                      stream, k8_map, page_map, half_map, p, k_scale, int(num_pages));
 }
 
 }  // namespace pagedmla

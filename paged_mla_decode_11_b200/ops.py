@@ -402,10 +402,16 @@ def mla_decode_paged_fp8_rows(q: torch.Tensor, k8: torch.Tensor, k_scale: torch.
                               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                               skip_combine: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
     """mla_decode_paged_fp8 for any number of query rows per latent head (above 16 a CTA-pair
-    tensor-core kernel on the codes themselves)."""
+    tensor-core kernel on the codes themselves).  Without ``workspace`` the (device, stream)'s
+    scratch buffer is used, under CUDA-graph capture one that belongs to the graph."""
     if workspace is None and q.dim() == 4 and k8.dim() == 4 and tile_metadata.dim() == 2 and q.is_cuda:
         b, s_q, h_q, _ = q.shape
-        workspace = _default_workspace(workspace_size(b, s_q, h_q, k8.shape[2], tile_metadata.shape[0]), q.device)
+        nbytes = workspace_size(b, s_q, h_q, k8.shape[2], tile_metadata.shape[0])
+        if torch.cuda.is_current_stream_capturing():  # a graph's own: graphs may run side by side
+            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
+            workspace[:256].zero_()
+        else:
+            workspace = _default_workspace(nbytes, q.device)
     return (_binding or load_binding()).decode_fp8_rows(q, k8, k_scale, block_table, cache_seqlens, dv, tile_metadata,
                                                         num_splits, softmax_scale, causal, workspace, out, lse,
                                                         skip_combine)

@@ -228,6 +228,40 @@ def test_captured_and_replayed():
         assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
 
 
+def test_two_graphs_side_by_side():
+    # captured without a workspace: each graph has its own, so they may run at the same time
+    xs = [W.make_inputs_fp8(W.custom(5, 1, 128, 1, [3000, 1, 500, 64, 900], causal=True), seed=s) for s in (1, 2)]
+    runs = []
+    for x in xs:
+        ref, ref_lse, _ = run(x)
+        d = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in x.items()}
+        tile, splits = ops.get_mla_metadata(d["cache_seqlens"], 128, 1)
+        call = lambda: ops.mla_decode_paged_fp8_rows(d["q"], d["k8"], d["k_scale"], d["block_table"], d["cache_seqlens"],
+                                                     512, tile, splits, softmax_scale=x["softmax_scale"], causal=True)
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(8):
+                got = call()
+        runs.append((graph, got, ref, ref_lse, d, tile, splits, torch.cuda.Stream()))
+    for _ in range(5):
+        for graph, *_, stream in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, got, ref, ref_lse, *_ in runs:
+        assert torch.equal(got[0], ref) and torch.equal(got[1], ref_lse)
+
+
+def test_pages_outside_the_pool_leave_other_sequences_alone():
+    x = W.make_inputs_fp8(W.custom(3, 1, 128, 1, [200, 300, 64], causal=True), seed=4)
+    out, lse, _ = run(x)
+    x["block_table"][1, 2], x["block_table"][1, 3] = 1 << 30, -7
+    out2, lse2, _ = run(x)
+    assert torch.equal(out2[[0, 2]], out[[0, 2]]) and torch.equal(lse2[[0, 2]], lse[[0, 2]])
+
+
 @pytest.mark.parametrize("name", ["compute_bound", "causal_mtp", "skewed"])
 def test_full_size_workloads(name):
     w = W.WORKLOADS[name]
