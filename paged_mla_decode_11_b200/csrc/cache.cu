@@ -9,8 +9,12 @@
 //
 // Read: the rows of listed slots, in list order, as bf16 (codes times their scale).
 //
-// Both move each byte once and are bound by HBM.  Rows with a slot outside the pool are skipped
-// by the write and read as zeros.
+// Both move each byte once, so HBM bounds a long call and the launch a short one.  Rows with a slot
+// outside the pool are skipped by the write and read as zeros.
+//
+// Measured (B200, graphs of back-to-back calls, scattered slots): write of 64 rows 2.0 us (bf16) and 2.3
+// us (FP8); of 65,521 rows into the FP8 cache (114 MB) 24.5 us, 0.71 of the copy rate.  Read of 7,777
+// bf16 rows (18 MB) 3.8 us; of 65,521 FP8 rows (114 MB) 20.1 us, 0.86 of the copy rate.
 #include <cuda_fp8.h>
 
 #include "launch.h"
@@ -62,9 +66,12 @@ cudaError_t launch_cache_slots(const int32_t *row_ptr, const int32_t *seqlens, i
 // Write: one warp per row.  Lane l holds 16 latent columns in 16-byte accesses of neighbouring
 // lanes, and pair l of the rope columns, so the norm, the scale and the rotation need no shared
 // memory: two warp reductions per row.  A long call is bound by the instructions of the row's
-// arithmetic, not by its bytes: a warp therefore takes several rows, keeps the weight and its
-// pair's frequency in registers and reads the next row while it works on this one; products run
-// two to an instruction; and a row is divided by its scale with one division (below).
+// arithmetic (about 270 a row, issue slots 58% busy), not by its bytes: a warp therefore takes
+// several rows, keeps the weight and its pair's frequency in registers while cp.async brings the next
+// rows to shared memory; products run two to an instruction; and a row is divided by its scale with
+// one division (below).  65,521 rows: 43 us with a warp per row and 18 divisions, 34 us with rows in a
+// loop and the next one in registers, 24.5 us with the ring (25.2 us four rows deep, 30 us at 8 blocks
+// an SM, whose 64 registers spill).
 // ------------------------------------------------------------------------------------
 constexpr int kWriteWarps = 4, kWriteBlocks = 7;  // warps a block, blocks an SM
 constexpr int kWriteAhead = 3;                     // rows of a warp in shared memory
