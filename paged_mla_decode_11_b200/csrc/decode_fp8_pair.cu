@@ -28,16 +28,20 @@
 // output in tensor memory: the partner's load and the softmax of a group hide behind the next two
 // groups' scores.
 //
-// Measured (B200): 128 sequences x 128 heads x 4,096 tokens 152 us in short runs (960 TFLOP/s of the
-// formula's flops) and 179 us under the sustained power cap (SM clock 1.6 GHz); the bf16 kernel takes 195
-// to 205 us.  A group takes 2.25 us, its MMAs 1.41 us (36 score MMAs of 45 cycles, 16 of 67): the ring's
-// round trip bounds it (own page 1.5 us from issue to full, score 0.8, partner half or softmax 1.7, PV 0.6,
-// release and next issue 0.6, over three stages), and under the cap the power of the MMAs and the clock.
-// Kept on the way from 284 us with plan and combine: eight softmax warps instead of four, issue warps
-// that run converged so that descriptors stay uniform (an MMA issued from a divergent lane took 100
-// cycles instead of 45), barriers polled together, six query loaders that split ahead, output rows
-// transposed between lanes before they are stored.  Measured slower: register splits for the loaders
-// (setmaxnreg, which spilled), all warps loading the first query, one-lane polls, an L2 prefetch.
+// Measured (B200): 128 sequences x 128 heads x 4,096 tokens 150 us in short runs (970 TFLOP/s of the
+// formula's flops) and 177 us under the sustained power cap (SM clock 1.6 GHz), where the products'
+// energy sets the clock; the bf16 kernel takes 195 to 205 us.  A group takes about 3,700 cycles, of which
+// its products are issued in 2,250 (36 of the score at 37 cycles, 16 of PV at 56) and two gaps of
+// 600 to 700 lie between a group's score and the PV before it: with the pages in L2, or with a softmax
+// that rescales nothing, a group takes as long.  Kept on the way from 284 us with plan and combine: eight
+// softmax warps instead of four, issue warps that run converged so that descriptors stay uniform (an
+// MMA issued from a divergent lane took 100 cycles instead of 45), barriers polled together, six query
+// loaders that split ahead, output rows transposed between lanes before they are stored, the A tile of
+// PV kept in the operand buffer for its second half and the scales in registers (sustained, with the
+// combine, 193.8 to 191.6 to 190.5 us).  Measured slower: register splits for the loaders (setmaxnreg,
+// which spilled), all warps loading the first query, one-lane polls, an L2 prefetch, a fixed order of
+// score and PV with blocking waits (206), barriers polled between the MMAs (204), paired fp32 arithmetic
+// in the softmax (194.5), looped instead of unrolled MMAs (198).
 //
 // Shared memory (per CTA, 8 KB blocks of 64 rows x 128 bytes, 128-byte swizzle):
 //   ring: 3 stages x 6 slots: slots 0-4 the own page's column blocks; after the score CTA 0 reloads
@@ -157,6 +161,18 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, 
       "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Two products of one A tile, d0 by b0 and d1 by b1: the first keeps A in the tensor cores' operand
+// buffer for the second, which saves a third of its reads of shared memory.
+__device__ __forceinline__ void mma_f8_pair_twice(uint32_t d0, uint32_t d1, uint64_t a, uint64_t b0, uint64_t b1,
+                                                  uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %6, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f8f6f4.collector::a::fill [%0], %2, %3, %5, p;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f8f6f4.collector::a::lastuse [%1], %2, %4, %5, p;\n\t}" ::"r"(d0),
+      "r"(d1), "l"(a), "l"(b0), "l"(b1), "r"(idesc), "r"(acc)
       : "memory");
 }
 
@@ -527,14 +543,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
           const uint64_t vb = smem_desc_sw128(slot(st, 0), T::kBlock, 1024);
           for (int h = 0; h < halves; ++h)
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-              for (int v = 0; v < 2; ++v) {
-                const uint64_t a = uint64_t((h * 64 + ks * 32) >> 4);
-                const uint64_t b = vb + uint64_t(((2 * h + v) * T::kBlock + ks * 4096) >> 4);
-                mma_f8_pair(tmem + T::kTmemO + 128 * v, hi + a, b, idesc_hi, (!first || h > 0 || ks > 0) ? 1u : 0u);
-                mma_f8_pair(tmem + T::kTmemO + 128 * v, lo + a, b, idesc_lo, 1u);
-              }
+            for (int ks = 0; ks < 2; ++ks) {
+              const uint64_t a = uint64_t((h * 64 + ks * 32) >> 4);
+              const uint64_t b0 = vb + uint64_t((2 * h * T::kBlock + ks * 4096) >> 4), b1 = b0 + uint64_t(T::kBlock >> 4);
+              const uint32_t o = tmem + T::kTmemO, acc = (!first || h > 0 || ks > 0) ? 1u : 0u;
+              mma_f8_pair_twice(o, o + 128, hi + a, b0, b1, idesc_hi, acc);
+              mma_f8_pair_twice(o, o + 128, lo + a, b0, b1, idesc_lo, 1u);
+            }
           commit_both(bar(T::EMPTY + st));
           if (wv.j + 1 == wv.ngroups) {
             commit_both(bar(T::OFULL));
@@ -627,6 +642,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
         if (left > 3) sb = max(sb, __float_as_uint(fabsf(mine.w)));
         const int e_new = max(e_used, int(__reduce_max_sync(0xffffffffu, sb) >> 23) - 126);
         const float f = pow2(6 - e_new);
+        float ks[32];  // the scales of this warp's keys, read while the score is still running
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 s = sc4[8 * quarter + i];
+          ks[4 * i] = s.x, ks[4 * i + 1] = s.y, ks[4 * i + 2] = s.z, ks[4 * i + 3] = s.w;
+        }
         ok = all_lanes(ok && mbar_wait(bar(T::SFULL + st), phase, abort, p.status, lim_ns));
         tc_fence_after();
         float sv[32];
@@ -636,12 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
         if (lane == 0) arrive_cluster(sfree + 8u * st);
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 s = sc4[8 * quarter + i];
-          const float ks[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sv[4 * i + k] *= ks[k];
-        }
+        for (int i = 0; i < 32; ++i) sv[i] *= ks[i];
         // keys at or past this row's limit get -inf (only partial groups need the test)
         const bool partial = __any_sync(0xffffffffu, key0 + 32 > lim);
         if (partial) {
@@ -675,14 +691,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
         float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 s = sc4[8 * quarter + i];
-          const float ks[4] = {s.x, s.y, s.z, s.w};
           float v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float e = fast_exp2(fmaf(sv[4 * i + k], rowf, nbase));
             s4[k] += e;
-            v[k] = e * (ks[k] * f);
+            v[k] = e * (ks[4 * i + k] * f);
           }
           if (partial) {  // the scale of a slot that is no key may be anything
 #pragma unroll
