@@ -407,7 +407,7 @@ MLA_API int mla_cache_slots(const int32_t *row_ptr, const int32_t *cache_seqlens
  * or NaN becomes a NaN code and does not enter the scale.
  *   latent, rope  device, `dtype` (MLA_DTYPE_*), element (t, h, c) at t * strides[0] + h *
  *                 strides[1] + c (for instance the two column ranges of one projection);
- *                 strides non-negative multiples of 8, 16-byte aligned
+ *                 strides non-negative multiples of 8, 16-byte aligned, apart from the cache
  *   norm_weight   device [512] of `dtype`, 16-byte aligned, or NULL: no norm
  *   positions, inv_freq [32], magnitude, flags (MLA_ROPE_HALF, MLA_ROPE_POS64): as in mla_rope;
  *                 inv_freq NULL: the rope columns are stored as they are (positions unused)

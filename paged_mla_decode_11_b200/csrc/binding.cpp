@@ -277,6 +277,7 @@ PyObject *cache_write(PyObject *const *a, Py_ssize_t n) {
   need_vector(slots, "slots", "tokens", T);
   need_pool(pool, scale);
   if (pool.size(2) != h_kv) refuse_value("the cache and latent disagree on h_kv");
+  if (overlap(pool, latent) || overlap(pool, rp)) refuse_value("latent and rope must not overlap the cache");
   if (weight) {
     need_type(*weight, "norm_weight", latent.scalar_type());
     need_vector(*weight, "norm_weight", "512", kLatent);

@@ -636,8 +636,8 @@ def mla_cache_write(latent: torch.Tensor, rope: torch.Tensor, slots: torch.Tenso
                     interleaved: bool = True, magnitude: float = 1.0) -> None:
     """New tokens' latent rows into the cache k_cache [pages, 64, h_kv, 576] bf16 at ``slots``
     (int64 [T], page * 64 + offset, distinct; outside the pool: skipped).  latent [T, h_kv, 512]
-    and rope [T, h_kv, 64] are bf16, fp16 or fp32 with contiguous rows (views of one projection);
-    the latent is RMS-normalised when ``norm_weight`` [512] is given, the rope columns are turned
+    and rope [T, h_kv, 64] are bf16, fp16 or fp32 with contiguous rows (views of one projection,
+    not of the cache); the latent is RMS-normalised when ``norm_weight`` [512] is given, the rope columns are turned
     by ``positions`` [T] and ``inv_freq`` [32] when those are given (mla_rope)."""
     (_binding or load_binding()).cache_write(latent, rope, slots, k_cache, None, norm_weight, eps, positions, inv_freq,
                                              interleaved, magnitude)

@@ -125,6 +125,17 @@ def test_pool_refusals(call, over, exc, msg):
         fn(**a)
 
 
+def test_write_refuses_rows_of_the_cache_itself():
+    pool = z(3, 64, 1, 576)
+    rows = pool.view(192, 1, 576)[10:16]
+    for over in (dict(latent=rows[..., :512]), dict(rope=rows[..., 512:])):
+        with pytest.raises(ValueError, match="must not overlap the cache"):
+            ops.mla_cache_write(**write_args(k_cache=pool, **over))
+    with pytest.raises(ValueError, match="CUDA tensor"):       # other rows of the same storage
+        both = z(4, 64, 1, 576)
+        ops.mla_cache_write(**write_args(k_cache=both[:3], latent=both[3, :6, :, :512], rope=both[3, :6, :, 512:]))
+
+
 def test_read_refuses_an_output_inside_the_cache():
     pool = z(3, 64, 1, 576)
     with pytest.raises(ValueError, match="overlap the cache"):
