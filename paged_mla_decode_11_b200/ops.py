@@ -610,13 +610,36 @@ def rope_magnitude(factor: float, coefficient: float = 1.0) -> float:
     return 0.1 * coefficient * math.log(factor) + 1.0 if factor > 1.0 else 1.0
 
 
+class _Rope(torch.autograd.Function):
+    """mla_rope of an x that needs a gradient; the gradient is the rotation back."""
+
+    @staticmethod
+    def forward(ctx, x, positions, inv_freq, interleaved, magnitude, inverse):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.how = interleaved, magnitude, inverse
+        return (_binding or load_binding()).rope(x, positions, inv_freq, interleaved, magnitude, inverse, None)
+
+    @staticmethod
+    def backward(ctx, grad):
+        positions, inv_freq = ctx.saved_tensors
+        interleaved, magnitude, inverse = ctx.how
+        if grad.stride(-1) != 1:
+            grad = grad.contiguous()
+        return mla_rope(grad, positions, inv_freq, interleaved, magnitude, not inverse), None, None, None, None, None
+
+
 def mla_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool = True,
              magnitude: float = 1.0, inverse: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rotary positions on the last 2 * len(inv_freq) columns of x [T, H, D] (bf16, fp16 or fp32;
     last dim contiguous): pairs of columns (2i, 2i + 1), or (i, i + n) with ``interleaved=False``,
     turned by positions[t] * inv_freq[i] (int32 or int64 [T]; fp64 [n], rope_frequencies) and
     multiplied by ``magnitude``; the columns in front are copied.  ``inverse`` turns back, which is
-    also the gradient with respect to x.  ``out=x`` works in place."""
+    also the gradient with respect to x (recorded where x needs one; ``out`` is refused there).
+    ``out=x`` works in place."""
+    if torch.is_grad_enabled() and getattr(x, "requires_grad", False):
+        if out is not None:
+            raise ValueError("out cannot be given for an x that needs a gradient")
+        return _Rope.apply(x, positions, inv_freq, interleaved, magnitude, inverse)
     return (_binding or load_binding()).rope(x, positions, inv_freq, interleaved, magnitude, inverse, out)
 
 

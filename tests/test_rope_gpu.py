@@ -134,6 +134,68 @@ def test_inverse_is_the_gradient_and_undoes_the_rotation():
     assert ((back - x).abs() <= 2e-6 * (x.abs().amax(-1, keepdim=True) * 2)).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("inverse", [True, False])
+def test_gradient_is_recorded(dtype, interleaved, inverse):
+    """Through autograd: the gradient of sum(w * mla_rope(x)) is w turned the other way (the
+    formula's, within check's tolerance), also of gradients that arrive as expanded views and into
+    an x shared by all heads, whose gradient is the heads' sum."""
+    x, pos = draw(37, 6, 96, dtype, seed=3)
+    w, _ = draw(37, 6, 96, dtype, seed=4)
+    freq = ops.rope_frequencies(64, device="cuda")
+    how = (interleaved, 1.25, inverse)
+    leaf = x.clone().requires_grad_()
+    y = ops.mla_rope(leaf, pos, freq, *how)
+    assert y.requires_grad and torch.equal(y.detach(), ops.mla_rope(x, pos, freq, *how))
+    y.backward(w)
+    check(w, pos, freq, leaf.grad, interleaved, 1.25, not inverse)
+
+    leaf = x.clone().requires_grad_()
+    ops.mla_rope(leaf, pos, freq, *how).sum().backward()      # the gradient arrives with strides 0
+    check(torch.ones_like(x), pos, freq, leaf.grad, interleaved, 1.25, not inverse)
+
+    if dtype == torch.float32:
+        one = x[:, :1].clone().requires_grad_()
+        ops.mla_rope(one.expand(-1, 6, -1), pos, freq, *how).backward(w)
+        ref, size = rotated(w, pos, freq, interleaved, 1.25, not inverse)
+        # each head's gradient as in check, and five sums of fp32 (2^-24 of the heads' sum of sizes each)
+        each = 2.0 ** -24 * ref.abs() + 5e-7 * 1.25 * size
+        tol = each.sum(1, keepdim=True) + 5 * 2.0 ** -24 * (ref.abs() + each).sum(1, keepdim=True)
+        assert ((one.grad.double() - ref.sum(1, keepdim=True)).abs() <= tol).all()
+
+    with torch.no_grad():
+        assert not ops.mla_rope(leaf, pos, freq, *how).requires_grad
+
+
+def test_second_gradient_and_captured_backward():
+    """The gradient is linear in its input and recorded itself: turning forth, back and forth again.
+    A forward and backward pass captured in a graph gives what the eager one gives."""
+    x, pos = draw(9, 3, 64, torch.float32, seed=5)
+    w, _ = draw(9, 3, 64, torch.float32, seed=6)
+    freq = ops.rope_frequencies(64, device="cuda")
+    leaf, wl = x.clone().requires_grad_(), w.clone().requires_grad_()
+    (gx,) = torch.autograd.grad(ops.mla_rope(leaf, pos, freq), leaf, wl, create_graph=True)
+    (gw,) = torch.autograd.grad(gx, wl, x)
+    assert torch.equal(gw, ops.mla_rope(x, pos, freq))
+    eager = gx.detach().clone()
+    del leaf, gx, gw
+
+    static = x.clone().requires_grad_()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        torch.autograd.grad(ops.mla_rope(static, pos, freq), static, w)
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        (grad,) = torch.autograd.grad(ops.mla_rope(static, pos, freq), static, w)
+    grad.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(grad, eager)
+
+
 def test_non_finite_values_stay_in_their_pair():
     x, pos = draw(4, 2, 64, torch.float32, seed=6)
     clean = ops.mla_rope(x, pos, ops.rope_frequencies(64, device="cuda"))

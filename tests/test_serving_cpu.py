@@ -52,6 +52,18 @@ def test_rope_refusals(over, exc, msg):
         ops.mla_rope(**rope_args(**over))
 
 
+def test_rope_with_a_gradient_refuses_an_output_and_checks_alike():
+    x = z(5, 4, 64).requires_grad_()
+    with pytest.raises(ValueError, match="needs a gradient"):
+        ops.mla_rope(**rope_args(x=x, out=z(5, 4, 64)))
+    with pytest.raises(ValueError, match="positions"):
+        ops.mla_rope(**rope_args(x=x, positions=z(4, dtype=i64)))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        ops.mla_rope(**rope_args(x=x))
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):   # passes the checks
+        ops.mla_rope(**rope_args(x=x, out=z(5, 4, 64)))
+
+
 def test_rope_refuses_partly_overlapping_rows():
     base = z(5, 4, 200)
     with pytest.raises(ValueError, match="must not overlap it"):
