@@ -40,8 +40,8 @@
 // PV kept in the operand buffer for its second half and the scales in registers (sustained, with the
 // combine, 193.8 to 191.6 to 190.5 us).  Measured slower: register splits for the loaders (setmaxnreg,
 // which spilled), all warps loading the first query, one-lane polls, an L2 prefetch, a fixed order of
-// score and PV with blocking waits (206), barriers polled between the MMAs (204), paired fp32 arithmetic
-// in the softmax (194.5), looped instead of unrolled MMAs (198).
+// score and PV with blocking waits (206), barriers polled between the MMAs (204), score and PV issued
+// by two warps (198), paired fp32 arithmetic in the softmax (194.5), looped instead of unrolled MMAs (198).
 //
 // Shared memory (per CTA, 8 KB blocks of 64 rows x 128 bytes, 128-byte swizzle):
 //   ring: 3 stages x 6 slots: slots 0-4 the own page's column blocks; after the score CTA 0 reloads
