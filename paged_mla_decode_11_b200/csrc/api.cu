@@ -764,8 +764,9 @@ int mla_rope(const void *x, const int64_t x_strides[2], int dtype, int64_t token
   if (tokens < 0 || heads < 1) return fail(MLA_ERR_ARG, "tokens must be >= 0 and heads >= 1");
   int rc = check_dtype(dtype);
   if (rc) return rc;
-  if (pairs < 1 || pairs > 512 || width < 2 * pairs || width > 65536)
-    return fail(MLA_ERR_ARG, "pairs must be in [1, 512] and width in [2 * pairs, 65536] (got %d, %d)", pairs, width);
+  if (pairs < 1 || pairs > kRopeMaxPairs || width < 2 * pairs || width > 65536)
+    return fail(MLA_ERR_ARG, "pairs must be in [1, %d] and width in [2 * pairs, 65536] (got %d, %d)", kRopeMaxPairs, pairs,
+                width);
   if (flags & ~(MLA_ROPE_HALF | MLA_ROPE_INVERSE | MLA_ROPE_POS64)) return fail(MLA_ERR_ARG, "unknown flags 0x%x", flags);
   if (!std::isfinite(magnitude)) return fail(MLA_ERR_ARG, "magnitude must be finite");
   if (tokens == 0) return MLA_OK;

@@ -56,6 +56,7 @@ cudaError_t launch_absorb_out(const __nv_bfloat16 *o_lat, int64_t l_row, int64_t
                               __nv_bfloat16 *out, int T, int H, cudaStream_t stream);
 
 // Rotary positions (rope.cu); strides in elements, the tile sizes are the launcher's.
+constexpr int kRopeMaxPairs = 512;
 struct RopeParams {
   const void *x;
   void *out;

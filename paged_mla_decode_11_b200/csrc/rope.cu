@@ -24,12 +24,16 @@ namespace pagedmla {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxAngles = 1024;  // per block (8 KB of shared memory)
 
-// Each unit is VEC pairs, two accesses of VEC elements; a tile has at most kRopeUnits of them a
-// thread.  The units are read first, so that the angles are computed while they are on their way.
-constexpr int kRopeUnits = 1;
+// Each unit is VEC pairs, two accesses of VEC elements.  A tile has one of them a thread, or the units
+// of a single row where those are more: with kRopeMaxPairs pairs moved one at a time two a thread.  The
+// units are read first, so that the angles are computed while they are on their way.
+template <int VEC>
+constexpr int kRopeUnits = (kRopeMaxPairs / VEC + kRopeThreads - 1) / kRopeThreads;
 
 template <typename T, bool kHalf, int VEC>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  static_assert(kRopeMaxPairs <= kRopeMaxAngles, "the angles of one token fit");
+  constexpr int kUnits = kRopeUnits<VEC>;
   __shared__ float2 cs[kRopeMaxAngles];
   using V = Pack<T, VEC>;
   const int64_t t0 = int64_t(blockIdx.x) * p.tile_tokens;
@@ -42,7 +46,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const T *x = static_cast<const T *>(p.x);
   T *out = static_cast<T *>(p.out);
   const int total = nt * nh * units;
-  V a[kRopeUnits], b[kRopeUnits];
+  V a[kUnits], b[kUnits];
   auto place = [&](int i, int &lt, int &h, int &u, int &c0, int &c1) {
     const int r = i / units;
     u = i - r * units;
@@ -52,7 +56,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     c1 = kHalf ? c0 + n : c0 + VEC;
   };
 #pragma unroll
-  for (int k = 0; k < kRopeUnits; ++k) {
+  for (int k = 0; k < kUnits; ++k) {
     const int i = threadIdx.x + k * kRopeThreads;
     if (i < total) {
       int lt, h, u, c0, c1;
@@ -78,7 +82,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
                          p.magnitude, p.inverse);
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kRopeUnits; ++k) {
+  for (int k = 0; k < kUnits; ++k) {
     const int i = threadIdx.x + k * kRopeThreads;
     if (i >= total) break;
     int lt, h, u, c0, c1;
@@ -114,11 +118,10 @@ cudaError_t launch_rope(RopeParams p, int dtype, bool half, cudaStream_t stream)
   const bool wide = multiple(p.pairs) && multiple(p.width) && multiple(p.x_t) && multiple(p.x_h) && multiple(p.o_t) &&
                     multiple(p.o_h) && reinterpret_cast<uintptr_t>(p.x) % 16 == 0 &&
                     reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
-  // a tile of heads, then of tokens, of at most kRopeUnits units a thread (pairs <= 512 fit alone)
+  // a tile of heads, then of tokens, of one unit a thread, but of a row at least
   const int units = wide ? p.pairs / vec : p.pairs;
-  const int target = kRopeUnits * kRopeThreads;
-  p.tile_heads = std::max(1, std::min(p.heads, target / units));
-  p.tile_tokens = std::max(1, std::min(target / (units * p.tile_heads), kRopeMaxAngles / p.pairs));
+  p.tile_heads = std::max(1, std::min(p.heads, kRopeThreads / units));
+  p.tile_tokens = std::max(1, std::min(kRopeThreads / (units * p.tile_heads), kRopeMaxAngles / p.pairs));
   switch (dtype) {
     case MLA_DTYPE_BF16:
       return half ? launch_rope_typed<__nv_bfloat16, true>(p, wide, stream)

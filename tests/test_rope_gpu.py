@@ -255,3 +255,32 @@ def test_frequencies_are_the_formulas():
     assert ntk[0] == 1.0 and math.isclose(ntk[-1], f[-1] / 8, rel_tol=1e-12)
     yarn = ops.rope_frequencies(64, scaling="yarn", factor=40.0)
     assert math.isclose(yarn[0], f[0]) and math.isclose(yarn[-1], f[-1] / 40) and (yarn <= f).all() and (yarn >= f / 40 * (1 - 1e-12)).all()
+
+
+@pytest.mark.parametrize("n", [256, 257, 300, 511, 512])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_wide_rotations_element_by_element(n, dtype, interleaved):
+    """Rows that cannot be moved 16 bytes at a time: an odd width, an odd row stride and an odd offset;
+    into an output that held NaN, in place and as the gradient."""
+    freq = ops.rope_frequencies(2 * n, device="cuda")
+    how = dict(interleaved=interleaved, magnitude=1.25)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    odd_width, pos = draw(3, 2, 2 * n + 3, dtype, seed=n)
+    odd_stride = torch.randn(3, 2, 2 * n + 1, generator=g, device="cuda").to(dtype)[..., :2 * n]
+    odd_offset = torch.randn(3, 2, 2 * n + 8, generator=g, device="cuda").to(dtype)[..., 1:1 + 2 * n]
+    for x in (odd_width, odd_stride, odd_offset):
+        out = torch.full_like(x, float("nan"))
+        ops.mla_rope(x, pos, freq, out=out, **how)
+        check(x, pos, freq, out, **how)
+        check(x, pos, freq, ops.mla_rope(x, pos, freq, **how), **how)
+        kept = torch.full((3, 2, 2 * n + 9), 7.0, dtype=dtype, device="cuda")
+        place = kept[..., 1:1 + x.shape[-1]]
+        place.copy_(x)
+        ops.mla_rope(place, pos, freq, out=place, **how)
+        assert torch.equal(place, out)
+        assert (kept[..., :1] == 7).all() and (kept[..., 1 + x.shape[-1]:] == 7).all()
+        leaf = x.clone().requires_grad_()
+        w = torch.empty(3, 2, 2 * n + 9, dtype=dtype, device="cuda")[..., 1:1 + x.shape[-1]].copy_(x.flip(0))
+        ops.mla_rope(leaf, pos, freq, **how).backward(w)
+        check(w, pos, freq, leaf.grad, inverse=True, **how)
