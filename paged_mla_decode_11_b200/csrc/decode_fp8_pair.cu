@@ -8,11 +8,14 @@
 //                             nearest E4M3 value and q_lo, E4M3, the rest.  A bf16 value has 8
 //                             significant bits and E4M3 4: the sum is exact for every |q| above
 //                             2^-10 of the row's largest, below it is off by at most 2^-18 of that
-//   P s 2^(6-e) = v_hi + v_lo  s the key's scale, 2^e above every scale of the piece so far: v_hi the
-//                             nearest E4M3 value, v_lo the rest in E5M2.  For v in [2^k, 2^(k+1)) the
-//                             rest is at most 2^(k-4) and E5M2's half step below that 2^(k-8): within
-//                             2^-8 of the value, as a bf16 rounding of P is, while v >= 2^-6; below,
-//                             within 2^-14, that is 2^-20 of the row's largest
+//   P s = 2^u (v_hi + v_lo)  s the key's scale, u the row's own: its largest P s so far is in [2^6, 2^8]
+//                             units.  v_hi is the nearest E4M3 value, v_lo the rest in E5M2.  For v in
+//                             [2^k, 2^(k+1)) the rest is at most 2^(k-4) and E5M2's half step below that
+//                             2^(k-8): within 2^-8 of the value, as a bf16 rounding of P is, while
+//                             v >= 2^-6; below, within 2^-14, that is 2^-20 of the row's largest.  (A
+//                             unit of the largest scale alone would let a key of no weight in the row,
+//                             such as a row of zeros, which the writer stores with scale 1, push all
+//                             others below 2^-14)
 // so S = (q_hi K^T + q_lo K^T) 2^-a s and O = v_hi V + v_lo V take twice the products at twice the
 // bf16 rate, on half the bytes.  Sums are fp32 in tensor memory.
 //
@@ -32,8 +35,8 @@
 // formula's flops) and 177 us under the sustained power cap (SM clock 1.6 GHz), where the products'
 // energy sets the clock; the bf16 kernel takes 195 to 205 us.  A group takes about 3,700 cycles, of which
 // its products are issued in 2,250 (36 of the score at 37 cycles, 16 of PV at 56) and two gaps of
-// 600 to 700 lie between a group's score and the PV before it: with the pages in L2, or with a softmax
-// that rescales nothing, a group takes as long.  Kept on the way from 284 us with plan and combine: eight
+// 600 to 700 lie between a group's score and the PV before it; with the pages in L2 a group takes as long.
+// Kept on the way from 284 us with plan and combine: eight
 // softmax warps instead of four, issue warps that run converged so that descriptors stay uniform (an
 // MMA issued from a divergent lane took 100 cycles instead of 45), barriers polled together, six query
 // loaders that split ahead, output rows transposed between lanes before they are stored, the A tile of
@@ -42,6 +45,10 @@
 // which spilled), all warps loading the first query, one-lane polls, an L2 prefetch, a fixed order of
 // score and PV with blocking waits (206), barriers polled between the MMAs (204), score and PV issued
 // by two warps (198), paired fp32 arithmetic in the softmax (194.5), looped instead of unrolled MMAs (198).
+// The unit of v by row (see above) costs 2.7% against one of the largest scale (with plan and combine, in
+// turn, 170.8 -> 175.4 us; 33 ragged sequences of two tokens 68.0 -> 71.2); rescaling O takes 4% of either.  The
+// score's maxima and the largest P s exchanged one after the other took 180.2, both behind a barrier
+// that tells whether any thread needs them 178.8 to 211.
 //
 // Shared memory (per CTA, 8 KB blocks of 64 rows x 128 bytes, 128-byte swizzle):
 //   ring: 3 stages x 6 slots: slots 0-4 the own page's column blocks; after the score CTA 0 reloads
@@ -625,23 +632,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
       // score of raw products to log2 units: 2^-a of the row and the softmax scale
       // (kept above 0, so that a masked score stays -inf)
       const float rowf = fmaxf(qscale[(qs & (T::kQScales - 1)) * 64 + lrow] * p.scale_log2, 1.2e-38f);
-      float m_used = -INFINITY, l = 0.f;  // l: this thread's quarter of the row sum
-      int e_used = -100;                  // every key scale of the piece so far is below 2^e_used
+      float m_used = -INFINITY, l = 0.f;  // of this thread's quarter of the row's keys: maximum, sum of P
+      float unit = -INFINITY;             // log2 of the row's unit of v and O
       for (int j = 0; j < w.ngroups; ++j, ++g) {
         ok = all_lanes(ok && mbar_wait(bar(T::SCALES + st), phase, abort, p.status, lim_ns));
         const float4 *sc4 = reinterpret_cast<const float4 *>(smem + T::kOffSc + st * 512);
-        const int group0 = w.t0 + 128 * j, key0 = group0 + 32 * quarter;
-        // the largest scale of the group's keys, the same in every thread of the pair; slots past the
-        // piece's end are not keys and their scales are never used
-        const float4 mine = sc4[lane];
-        const int left = w.t1 - (group0 + 4 * lane);
-        uint32_t sb = 0;
-        if (left > 0) sb = __float_as_uint(fabsf(mine.x));
-        if (left > 1) sb = max(sb, __float_as_uint(fabsf(mine.y)));
-        if (left > 2) sb = max(sb, __float_as_uint(fabsf(mine.z)));
-        if (left > 3) sb = max(sb, __float_as_uint(fabsf(mine.w)));
-        const int e_new = max(e_used, int(__reduce_max_sync(0xffffffffu, sb) >> 23) - 126);
-        const float f = pow2(6 - e_new);
+        const int key0 = w.t0 + 128 * j + 32 * quarter;
         float ks[32];  // the scales of this warp's keys, read while the score is still running
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -658,54 +654,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < 32; ++i) sv[i] *= ks[i];
-        // keys at or past this row's limit get -inf (only partial groups need the test)
-        const bool partial = __any_sync(0xffffffffu, key0 + 32 > lim);
-        if (partial) {
+        // keys at or past this row's limit get -inf, and no scale: that of a slot that is no key may be
+        // anything (only partial groups need the test)
+        if (__any_sync(0xffffffffu, key0 + 32 > lim)) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (key0 + i >= lim) sv[i] = -INFINITY;
+            if (key0 + i >= lim) {
+              sv[i] = -INFINITY;
+              ks[i] = 0.f;
+            }
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], sv[i]);
-        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rowf;
-        // the row's other keys live on the partner warps: exchange maxima
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rowf;
+        // The quarter's own running maximum, refreshed when it grows by more than 2 (log2 units).  P is
+        // taken a quarter of its size: it stays below 1, and P s below the scale
+        const float m_new = mx > m_used + 2.f ? mx : m_used;
+        l *= m_new > m_used ? fast_exp2(m_used - m_new) : 1.f;
+        m_used = m_new;
+        const float nbase = m_used == -INFINITY ? 0.f : -2.f - m_used;
+        float s4[4] = {0.f, 0.f, 0.f, 0.f}, t4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float e = fast_exp2(fmaf(sv[i], rowf, nbase));
+          s4[i & 3] += e;
+          sv[i] = e * ks[i];
+          if (i & 1) t4[(i >> 1) & 3] = fmaxf(t4[(i >> 1) & 3], fmaxf(fabsf(sv[i - 1]), fabsf(sv[i])));
+        }
+        // The quarters share the unit of v, which follows the row's largest P s: exchange those.  It is
+        // refreshed when that leaves 2^8 units, which E4M3 still holds, and then put at 2^6.  A unit is at
+        // least 2^-118 of the largest P, which holds scales down to 2^-110 and keeps f finite
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         float *xm = xmax + (g & 1) * 4 * 64 + lrow;
-        xm[quarter * 64] = mx;
+        xm[quarter * 64] = m_used + fmaxf(2.f + fast_log2(top), -112.f);
         named_bar_sync(xbar, 128);
-        mx = fmaxf(fmaxf(xm[0], xm[64]), fmaxf(xm[128], xm[192]));
-        // The running maximum is refreshed when it grows by more than 2 (log2 units), so P stays
-        // below 4 and v = P s 2^(6-e) below 256, inside E4M3
-        const float m_new = fmaxf(m_used, mx);
-        const bool need = m_new > m_used + 2.f;
+        l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        const float row_top = fmaxf(fmaxf(xm[0], xm[64]), fmaxf(xm[128], xm[192]));
+        const bool need = row_top > unit + 8.f;
         float alpha = 1.f;
         if (need) {
-          alpha = fast_exp2(m_used - m_new);
-          m_used = m_new;
+          alpha = fast_exp2(unit - (row_top - 6.f));
+          unit = row_top - 6.f;
         }
-        const float nbase = m_used == -INFINITY ? 0.f : -m_used;
-        l *= alpha;
-        const bool rescale = j > 0 && (__any_sync(0xffffffffu, need) || e_new > e_used);
-        alpha *= e_new - e_used < 127 ? pow2(-min(e_new - e_used, 126)) : 0.f;
-        e_used = e_new;
+        const bool rescale = j > 0 && __any_sync(0xffffffffu, need);
+        const float f = m_used == -INFINITY ? 0.f : fast_exp2(m_used + 2.f - unit);
         uint32_t hi[8], lo[8];
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float e = fast_exp2(fmaf(sv[4 * i + k], rowf, nbase));
-            s4[k] += e;
-            v[k] = e * (ks[4 * i + k] * f);
-          }
-          if (partial) {  // the scale of a slot that is no key may be anything
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (key0 + 4 * i + k >= lim) v[k] = 0.f;
-          }
+          const float v[4] = {sv[4 * i] * f, sv[4 * i + 1] * f, sv[4 * i + 2] * f, sv[4 * i + 3] * f};
           split_v(v, hi[i], lo[i]);
         }
-        l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
         // O may be rescaled once the previous group's PV has completed (its commit arrives on EMPTY
         // of that group's stage; that barrier is at most one phase behind)
         if (rescale) {
@@ -748,13 +746,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
       }
 
       // ---- epilogue: O / l -> output (or fp32 split partial), natural-log LSE ----
+      // (the buffer of the next group's maxima, last read before the barrier of the last group)
+      float *xm = xmax + (g & 1) * 4 * 64 + lrow;
+      xm[quarter * 64] = m_used;
       xsum[quarter * 64 + lrow] = l;
       named_bar_sync(xbar, 128);
-      const float l_row = (xsum[lrow] + xsum[64 + lrow]) + (xsum[128 + lrow] + xsum[192 + lrow]);
+      const float m_row = fmaxf(fmaxf(xm[0], xm[64]), fmaxf(xm[128], xm[192]));
+      float l_row = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // a quarter without a visible key has no sum, or that of a row of NaN
+        const float l_i = xsum[64 * i + lrow], m_i = xm[64 * i];
+        l_row += m_i == -INFINITY ? l_i : l_i * fast_exp2(m_i - m_row);
+      }
       ok = all_lanes(ok && mbar_wait(bar(T::OFULL), qs & 1, abort, p.status, lim_ns));
       tc_fence_after();
       if (ok) {
-        const float inv = l_row > 0.f ? pow2(e_used - 6) / l_row : (l_row == 0.f ? 0.f : l_row);
+        const float inv = l_row > 0.f ? fast_exp2(unit - m_row - 2.f) / l_row : (l_row == 0.f ? 0.f : l_row);
         const int64_t out_off = out_row - p.out;
 #pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += 32) {
@@ -793,7 +801,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FpPair::kThreads, 1)
           }
         }
         if (active && quarter == 0) {
-          const float lse_v = l_row == 0.f ? -INFINITY : (m_used + fast_log2(l_row)) * 0.69314718055994531f;
+          const float lse_v = l_row == 0.f ? -INFINITY : (m_row + 2.f + fast_log2(l_row)) * 0.69314718055994531f;
           if (nsplit == 1)
             *lse_row = lse_v;
           else

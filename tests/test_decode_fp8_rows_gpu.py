@@ -12,6 +12,8 @@ means p s < 2^-11 max(p) max(s), and 2^-14 is 2^-19 max(p) max(s).  Together at 
 (2^-8 + 1e-3) * sum_j p_j |c_j| + 2^-19 max(p) max(s) * (sum of |code_j| over those small ones).
 LSE: the library's 1e-4 of max(|lse|, 1)."""
 
+import math
+
 import pytest
 import torch
 
@@ -268,3 +270,106 @@ def test_full_size_workloads(name):
     x = W.make_inputs_fp8(w, seed=0)
     worst, lse = parity(x)
     print(f"{name} over the FP8 cache: out {worst:.3f} of its tolerance, lse {lse:.2e}")
+
+
+# --- keys whose scale is far above what they weigh -------------------------------------------------
+#
+# Tolerances relative to what each row holds itself.  The kernel's unit of v = P s follows the row's own
+# largest P s: it lies in [2^6, 2^8] of them.  So v >= 2^-6, where its two terms keep it within 2^-8 (and
+# its f16 form within 2^-11), for every key with p s >= 2^-12 of the row's largest; below, 2^-14 is at most
+# 2^-20 of the largest (2^-11 in the code, for the largest of a part of the sequence).  A query element is
+# exact when it is at least 2^-9 of its row's largest and within 2^-17 of the largest otherwise; each of
+# the 36 accumulations of a score rounds by at most 2^-23 of sum|q k|.  A score off by d moves its
+# probability by e^d, and all of them together.  2^-14 for the sums of PV (2^-23 for each of some 2^8
+# accumulations and rescalings) and the exponentials.
+def own_parity(x, num_parts=None):
+    out, lse, _ = run(x, num_parts)
+    q, h, g = x["q"].cuda().double(), x["h_kv"], x["h_q"] // x["h_kv"]
+    k8, ks = x["k8"].cuda().view(torch.uint8), x["k_scale"].cuda().double()
+    worst = 0.0
+    for i, L in enumerate(x["cache_seqlens"].tolist()):
+        pages = x["block_table"][i, :-(-L // 64)].long().cuda()
+        for n in range(h):
+            s = ks[n, pages].flatten()[:L]
+            codes = k8[pages, :, n].view(torch.float8_e4m3fn).float().double().flatten(0, 1)[:L]
+            c = codes * s[:, None]
+            qn = q[i, :, n * g:(n + 1) * g]                                                   # [s_q, g, 576]
+            top = qn.abs().amax(-1, keepdim=True)
+            off = torch.where((qn.abs() >= 2.0 ** -9 * top) | (qn == 0), 0.0, 2.0 ** -17 * top)
+            d = (off @ c.abs().t() + 36 * 2.0 ** -23 * (qn.abs() @ c.abs().t())) * x["softmax_scale"]
+            rows = qn @ c.t() * x["softmax_scale"]
+            if x["causal"]:
+                keep = torch.arange(L, device="cuda") < L - (x["s_q"] - 1 - torch.arange(x["s_q"], device="cuda"))[:, None]
+                rows = rows.masked_fill(~keep[:, None], -torch.inf)
+            z = torch.logsumexp(rows, -1)
+            p = torch.where(z[..., None] == -torch.inf, 0.0, (rows - z[..., None]).exp())
+            ref = p @ c[:, :512]
+            move = p * d.clamp_max(50).expm1()
+            small = (p * s < 2.0 ** -11 * (p * s).amax(-1, keepdim=True)).double()
+            tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -14) * (p @ c[:, :512].abs()) + \
+                move @ c[:, :512].abs() + move.sum(-1, keepdim=True) * ref.abs() + \
+                2.0 ** -20 * (p * s).amax(-1, keepdim=True) * (small @ codes[:, :512].abs()) + 1e-30
+            err = ((out[i, :, n * g:(n + 1) * g].double() - ref).abs() / tol).max()
+            worst = max(worst, float(err))
+            gone = z == -torch.inf
+            got = lse[i, n * g:(n + 1) * g].t().double()
+            assert torch.equal(got == -torch.inf, gone)
+            assert ((got - z).abs() <= 1e-4 * z.abs().clamp_min(1) + move.sum(-1))[~gone].all()
+    assert worst <= 1, f"out off by {worst:.3f} of the tolerance"
+    return worst
+
+
+def key_at(x, b, t):
+    return int(x["block_table"][b, t // 64]), t % 64
+
+
+@pytest.mark.parametrize("std", [1.0, 1e-2, 1e-4])
+@pytest.mark.parametrize("s_q,h_q", [(1, 17), (2, 64), (3, 64)])
+@pytest.mark.parametrize("num_parts", [None, 1])
+def test_rows_of_zeros_among_small_rows(std, s_q, h_q, num_parts):
+    # the writer stores a row of zeros with scale 1, hundreds of thousands of times a small row's
+    x = W.make_inputs(W.custom(3, s_q, h_q, 1, [1000, 130, 3], causal=True), seed=h_q + s_q)
+    x["k_cache"][:x["num_pages"]] *= std
+    x["q"] = (x["q"].float() / std).to(torch.bfloat16)
+    for b, t in ((0, 5), (0, 700), (1, 129), (2, 0)):          # 129: only the last position sees it
+        x["k_cache"][key_at(x, b, t)] = 0
+    x["k8"], x["k_scale"] = W.to_fp8_cache(x["k_cache"])
+    assert x["k_scale"][0][key_at(x, 1, 129)] == 1
+    own_parity(x, num_parts)
+
+
+@pytest.mark.parametrize("h_q", [17, 128])
+@pytest.mark.parametrize("num_parts", [None, 1])
+def test_large_keys_of_no_weight(h_q, num_parts):
+    # scores of -20,000: no probability, but scales 5,000 times the other keys'
+    x = W.make_inputs(W.custom(2, 1, h_q, 1, [600, 129], causal=False), seed=h_q)
+    x["q"][..., 0] = 8
+    for b, t in ((0, 17), (0, 40), (0, 300), (1, 0), (1, 128)):
+        row = x["k_cache"][key_at(x, b, t)]
+        row *= 2.0 ** 10
+        row[..., 0] = -2.0 ** 16
+    x["k8"], x["k_scale"] = W.to_fp8_cache(x["k_cache"])
+    own_parity(x, num_parts)
+
+
+@pytest.mark.parametrize("h_q,s_q", [(17, 1), (128, 1), (64, 3)])
+@pytest.mark.parametrize("num_parts", [None, 1])
+@pytest.mark.parametrize("span", [4, 8])
+def test_scales_against_probabilities(h_q, s_q, num_parts, span):
+    # scales 2^e with e up to +-span, and scores that fall with e: p s is spread by 2^(span / 2) both ways
+    # around one, led by large keys in some places and by small ones in others
+    x = W.make_inputs_fp8(W.custom(3, s_q, h_q, 1, [900, 190, 64], causal=True), seed=span + h_q)
+    g = torch.Generator().manual_seed(span)
+    n = x["k8"].shape[0]
+    e = torch.randint(-span, span + 1, (n, 64), generator=g).float()
+    e[: n // 2] = e[: n // 2].sort(-1).values                  # growing within a page, and any order
+    x["k_scale"] = torch.exp2(e)[None].contiguous()
+    score = -math.log(2.0) * e * (0.5 + torch.rand(n, 64, generator=g))
+    # only column 512 of the query is not zero: the score is q_512 * code_512 * scale / 24, and 2^(span - 1)
+    # in it reaches the scores of the smallest scales with codes below 448
+    x["softmax_scale"] = 1 / 24
+    x["q"].zero_()
+    x["q"][..., 512] = (0.75 + 0.5 * torch.rand(x["q"].shape[:3], generator=g)) * 2.0 ** (span - 1)
+    code = (24 * 2.0 ** (1 - span) * score / torch.exp2(e)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    x["k8"][:, :, 0, 512] = code
+    own_parity(x, num_parts)
