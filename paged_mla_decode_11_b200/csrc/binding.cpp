@@ -9,6 +9,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -92,6 +93,17 @@ bool overlap(const at::Tensor &a, const at::Tensor &b) {
   if (a.numel() == 0 || b.numel() == 0) return false;
   const char *a0 = static_cast<const char *>(a.const_data_ptr()), *b0 = static_cast<const char *>(b.const_data_ptr());
   return a0 < end(b) && b0 < end(a);
+}
+
+// A caller's tensor that the call writes: no gradient goes through that write ...
+void need_writable(const at::Tensor &t, const char *name) {
+  if (c10::GradMode::is_enabled() && t.requires_grad())
+    refuse_value(std::string(name) + " must not require a gradient: the call writes it");
+}
+
+// ... and autograd is told of it, so that a backward pass that saved the tensor raises.
+void written(const at::Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 // The device of a call: that of its first tensor, which the others must share.
@@ -179,6 +191,7 @@ PyObject *rope(PyObject *const *a, Py_ssize_t n) {
     const bool in_place = out->const_data_ptr() == x.const_data_ptr() && out->strides() == x.strides();
     if (!in_place && overlap(x, *out)) refuse_value("out must be x itself or must not overlap it");
     need_rows_apart(*out, "out");
+    need_writable(*out, "out");
   }
   const Place place(x, "x");
   place.same(positions, "positions");
@@ -194,7 +207,10 @@ PyObject *rope(PyObject *const *a, Py_ssize_t n) {
                       static_cast<const double *>(freq.const_data_ptr()), magnitude, flags, out->data_ptr(), os, stream);
     });
   }
-  if (given(a[6])) return Py_NewRef(a[6]);
+  if (given(a[6])) {
+    written(*out);
+    return Py_NewRef(a[6]);
+  }
   return THPVariable_Wrap(std::move(fresh));
 }
 
@@ -236,6 +252,8 @@ PyObject *cache_slots(PyObject *const *a, Py_ssize_t n) {
                            pages, tokens, static_cast<int64_t *>(out[0]->data_ptr()),
                            static_cast<int32_t *>(out[1]->data_ptr()), stream);
   });
+  for (int i = 0; i < 2; ++i)
+    if (given(a[5 + i])) written(*out[i]);
   PyObject *first = given(a[5]) ? Py_NewRef(a[5]) : THPVariable_Wrap(std::move(fresh[0]));
   PyObject *second = given(a[6]) ? Py_NewRef(a[6]) : THPVariable_Wrap(std::move(fresh[1]));
   return Py_BuildValue("(NN)", first, second);
@@ -278,6 +296,8 @@ PyObject *cache_write(PyObject *const *a, Py_ssize_t n) {
   need_pool(pool, scale);
   if (pool.size(2) != h_kv) refuse_value("the cache and latent disagree on h_kv");
   if (overlap(pool, latent) || overlap(pool, rp)) refuse_value("latent and rope must not overlap the cache");
+  need_writable(pool, "the cache");
+  if (scale) need_writable(*scale, "k_scale");
   if (weight) {
     need_type(*weight, "norm_weight", latent.scalar_type());
     need_vector(*weight, "norm_weight", "512", kLatent);
@@ -312,6 +332,8 @@ PyObject *cache_write(PyObject *const *a, Py_ssize_t n) {
                  : api.cache_write(latent.const_data_ptr(), ls, rp.const_data_ptr(), rs, type, T, int(h_kv), w, eps, pos, f,
                                    magnitude, flags, at, pool.data_ptr(), pool.size(0), int(pool.size(1)), stream);
   });
+  written(pool);
+  if (scale) written(*scale);
   Py_RETURN_NONE;
 }
 
@@ -333,6 +355,7 @@ PyObject *cache_read(PyObject *const *a, Py_ssize_t n) {
       refuse_value("out must be [tokens, h_kv, 576] with contiguous rows");
     need_rows_apart(*out, "out");
     if (overlap(pool, *out)) refuse_value("out must not overlap the cache");
+    need_writable(*out, "out");
   }
   const Place place(pool, "the cache");
   place.same(slots, "slots");
@@ -351,7 +374,10 @@ PyObject *cache_read(PyObject *const *a, Py_ssize_t n) {
                                     os, stream);
     });
   }
-  if (given(a[3])) return Py_NewRef(a[3]);
+  if (given(a[3])) {
+    written(*out);
+    return Py_NewRef(a[3]);
+  }
   return THPVariable_Wrap(std::move(fresh));
 }
 
@@ -439,11 +465,13 @@ PyObject *decode_fp8_rows(PyObject *const *a, Py_ssize_t n) {
     out = &tensor(a[11], "out");
     if (out->sizes() != at::IntArrayRef({b, s_q, h_q, dv}) || out->scalar_type() != at::kBFloat16 || !out->is_contiguous())
       refuse_value("out must be a contiguous bf16 [b, s_q, h_q, dv] tensor");
+    need_writable(*out, "out");
   }
   if (given(a[12])) {
     lse = &tensor(a[12], "lse");
     if (lse->sizes() != at::IntArrayRef({b, h_q, s_q}) || lse->scalar_type() != at::kFloat || !lse->is_contiguous())
       refuse_value("lse must be a contiguous fp32 [b, h_q, s_q] tensor");
+    need_writable(*lse, "lse");
   }
   const Place place(q, "q");
   place.same(k8, "k8");
@@ -471,6 +499,8 @@ PyObject *decode_fp8_rows(PyObject *const *a, Py_ssize_t n) {
         int(tile.size(0)), static_cast<const int32_t *>(splits.const_data_ptr()), softmax_scale, causal, out->data_ptr(),
         static_cast<float *>(lse->data_ptr()), workspace.data_ptr(), size_t(workspace.numel()), flags, stream);
   });
+  if (given(a[11])) written(*out);
+  if (given(a[12])) written(*lse);
   PyObject *first = given(a[11]) ? Py_NewRef(a[11]) : THPVariable_Wrap(std::move(fresh_out));
   PyObject *second = given(a[12]) ? Py_NewRef(a[12]) : THPVariable_Wrap(std::move(fresh_lse));
   return Py_BuildValue("(NN)", first, second);

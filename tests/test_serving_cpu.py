@@ -290,3 +290,23 @@ def test_frequency_refusals():
         with pytest.raises(ValueError):
             ops.rope_frequencies(**bad)
     assert ops.rope_magnitude(1.0) == 1.0 and math.isclose(ops.rope_magnitude(40.0), 0.1 * math.log(40.0) + 1)
+
+
+def test_written_tensors_that_need_a_gradient_are_refused():
+    grad = lambda t: t.requires_grad_()
+    calls = [
+        (ops.mla_rope, rope_args(out=grad(z(5, 4, 64))), "out must not require"),
+        (ops.mla_cache_write, write_args(k_cache=grad(z(3, 64, 1, 576))), "the cache must not require"),
+        (ops.mla_cache_write_fp8, write_args(True, k_scale=grad(z(1, 3, 64, dtype=f32))), "k_scale must not require"),
+        (ops.mla_cache_read, dict(k_cache=z(3, 64, 1, 576), slots=z(6, dtype=i64), out=grad(z(6, 1, 576))), "out must not require"),
+    ]
+    rows = dict(q=z(3, 1, 128, 576), k8=z(10, 64, 1, 576, dtype=torch.uint8), k_scale=z(1, 10, 64, dtype=f32),
+                block_table=z(3, 6, dtype=i32), cache_seqlens=z(3, dtype=i32), dv=512, tile_metadata=z(5, 8, dtype=i32),
+                num_splits=z(4, dtype=i32))
+    calls += [(ops.mla_decode_paged_fp8_rows, dict(rows, out=grad(z(3, 1, 128, 512))), "out must not require"),
+              (ops.mla_decode_paged_fp8_rows, dict(rows, lse=grad(z(3, 128, 1, dtype=f32))), "lse must not require")]
+    for fn, kw, msg in calls:
+        with pytest.raises(ValueError, match=msg):
+            fn(**kw)
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):      # passes the checks
+            fn(**kw)
