@@ -9,6 +9,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -165,6 +166,22 @@ bool truth(PyObject *o) {
   const int v = PyObject_IsTrue(o);
   if (v < 0) throw python_error();
   return v != 0;
+}
+
+// rope_recorded(x, inv_freq, out) -> whether autograd is to record the call: a gradient of x is wanted,
+// or x carries a tangent (forward mode).  Derivatives by the frequencies are refused, and an output.
+PyObject *rope_recorded(PyObject *const *a, Py_ssize_t n) {
+  need_arguments(n, 3);
+  const bool forward = c10::AutogradState::get_tls_state().get_fw_grad_mode(), backward = c10::GradMode::is_enabled();
+  auto differentiated = [&](PyObject *o) {
+    if (!THPVariable_Check(o)) return false;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    return (backward && t.requires_grad()) || (forward && t._fw_grad(0).defined());
+  };
+  if (differentiated(a[1])) refuse_value("the derivative by inv_freq is not formed: detach it");
+  if (!differentiated(a[0])) Py_RETURN_FALSE;
+  if (given(a[2])) refuse_value("out cannot be given for an x that needs a gradient");
+  Py_RETURN_TRUE;
 }
 
 // rope(x, positions, inv_freq, interleaved, magnitude, inverse, out)
@@ -550,6 +567,7 @@ PyMethodDef method(const char *name) {
 }
 
 PyMethodDef methods[] = {method<bind>("bind"),
+                         method<rope_recorded>("rope_recorded"),
                          method<rope>("rope"),
                          method<cache_slots>("cache_slots"),
                          method<cache_write>("cache_write"),

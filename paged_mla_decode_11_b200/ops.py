@@ -611,11 +611,13 @@ def rope_magnitude(factor: float, coefficient: float = 1.0) -> float:
 
 
 class _Rope(torch.autograd.Function):
-    """mla_rope of an x that needs a gradient; the gradient is the rotation back."""
+    """mla_rope of an x that needs a gradient or carries a tangent; the gradient is the rotation back,
+    the tangent the rotation."""
 
     @staticmethod
     def forward(ctx, x, positions, inv_freq, interleaved, magnitude, inverse):
         ctx.save_for_backward(positions, inv_freq)
+        ctx.save_for_forward(positions, inv_freq)
         ctx.how = interleaved, magnitude, inverse
         return (_binding or load_binding()).rope(x, positions, inv_freq, interleaved, magnitude, inverse, None)
 
@@ -627,6 +629,13 @@ class _Rope(torch.autograd.Function):
             grad = grad.contiguous()
         return mla_rope(grad, positions, inv_freq, interleaved, magnitude, not inverse), None, None, None, None, None
 
+    @staticmethod
+    def jvp(ctx, tangent, *_):
+        positions, inv_freq = ctx.saved_tensors
+        if tangent.stride(-1) != 1:
+            tangent = tangent.contiguous()
+        return mla_rope(tangent, positions, inv_freq, *ctx.how)
+
 
 def mla_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool = True,
              magnitude: float = 1.0, inverse: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -634,13 +643,12 @@ def mla_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, i
     last dim contiguous): pairs of columns (2i, 2i + 1), or (i, i + n) with ``interleaved=False``,
     turned by positions[t] * inv_freq[i] (int32 or int64 [T]; fp64 [n], rope_frequencies) and
     multiplied by ``magnitude``; the columns in front are copied.  ``inverse`` turns back, which is
-    also the gradient with respect to x (recorded where x needs one; ``out`` is refused there).
-    ``out=x`` works in place."""
-    if torch.is_grad_enabled() and getattr(x, "requires_grad", False):
-        if out is not None:
-            raise ValueError("out cannot be given for an x that needs a gradient")
+    also the gradient with respect to x (recorded where x needs one or carries a tangent; ``out`` is
+    refused there, and an ``inv_freq`` that is differentiated anywhere).  ``out=x`` works in place."""
+    native = _binding or load_binding()
+    if native.rope_recorded(x, inv_freq, out):
         return _Rope.apply(x, positions, inv_freq, interleaved, magnitude, inverse)
-    return (_binding or load_binding()).rope(x, positions, inv_freq, interleaved, magnitude, inverse, out)
+    return native.rope(x, positions, inv_freq, interleaved, magnitude, inverse, out)
 
 
 def mla_cache_slots(block_table: torch.Tensor, cache_seqlens: torch.Tensor, row_ptr: torch.Tensor, num_pages: int,

@@ -284,3 +284,31 @@ def test_wide_rotations_element_by_element(n, dtype, interleaved):
         w = torch.empty(3, 2, 2 * n + 9, dtype=dtype, device="cuda")[..., 1:1 + x.shape[-1]].copy_(x.flip(0))
         ops.mla_rope(leaf, pos, freq, **how).backward(w)
         check(w, pos, freq, leaf.grad, inverse=True, **how)
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("inverse", [True, False])
+def test_tangent_is_carried(interleaved, inverse):
+    """Forward mode: the map is linear, so the tangent is turned like x; also beside a gradient."""
+    import torch.autograd.forward_ad as fwd
+    x, pos = draw(9, 3, 80, torch.float32, seed=5)
+    t, _ = draw(9, 3, 80, torch.float32, seed=6)
+    w, _ = draw(9, 3, 80, torch.float32, seed=7)
+    freq = ops.rope_frequencies(64, device="cuda")
+    how = (interleaved, 1.25, inverse)
+    want, moved = ops.mla_rope(x, pos, freq, *how), ops.mla_rope(t, pos, freq, *how)
+    for tangent in (t, t.transpose(0, 2).contiguous().transpose(0, 2)):     # a strided last dimension
+        with fwd.dual_level():
+            out = fwd.unpack_dual(ops.mla_rope(fwd.make_dual(x, tangent), pos, freq, *how))
+            assert torch.equal(out.primal, want) and torch.equal(out.tangent, moved)
+    with fwd.dual_level(), torch.no_grad():
+        assert torch.equal(fwd.unpack_dual(ops.mla_rope(fwd.make_dual(x, t), pos, freq, *how)).tangent, moved)
+    leaf = x.clone().requires_grad_()
+    with fwd.dual_level():
+        out = fwd.unpack_dual(ops.mla_rope(fwd.make_dual(leaf, t), pos, freq, *how))
+        assert torch.equal(out.tangent, moved)
+        (grad,) = torch.autograd.grad(out.primal, leaf, w)
+    assert torch.equal(grad, ops.mla_rope(w, pos, freq, interleaved, 1.25, not inverse))
+    # differences of the formula: the tangent is that of the 64-bit map at any step
+    ref = rotated(t, pos, freq, *how)
+    assert ((moved.double() - ref[0]).abs() <= 2.0 ** -24 * ref[0].abs() + 5e-7 * 1.25 * ref[1]).all()

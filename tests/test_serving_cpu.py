@@ -310,3 +310,20 @@ def test_written_tensors_that_need_a_gradient_are_refused():
             fn(**kw)
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):      # passes the checks
             fn(**kw)
+
+
+def test_rope_refuses_what_it_cannot_differentiate():
+    import torch.autograd.forward_ad as fwd
+    freq = ops.rope_frequencies(64)
+    with pytest.raises(ValueError, match="derivative by inv_freq"):
+        ops.mla_rope(**rope_args(inv_freq=freq.clone().requires_grad_()))
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):
+        ops.mla_rope(**rope_args(inv_freq=freq.clone().requires_grad_()))
+    with fwd.dual_level():
+        with pytest.raises(ValueError, match="derivative by inv_freq"):
+            ops.mla_rope(**rope_args(inv_freq=fwd.make_dual(freq, torch.ones_like(freq))))
+        dual = fwd.make_dual(z(5, 4, 64), z(5, 4, 64))
+        with pytest.raises(ValueError, match="needs a gradient"):
+            ops.mla_rope(**rope_args(x=dual, out=z(5, 4, 64)))
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            ops.mla_rope(**rope_args(x=dual))
