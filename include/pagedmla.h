@@ -472,12 +472,27 @@ MLA_API int mla_cache_read_fp8(const void *k8, const float *k_scale, int64_t num
  *   tokens        device int32 [batch][drafts + 1], written: the accepted drafts, the next
  *                 token, then -1
  * drafts >= 1, vocab >= 1, strides >= 0, batch <= 2^24.  A programmatic dependent launch that
- * waits for the kernel before it.  Errors: MLA_ERR_ARG, MLA_ERR_CUDA.
+ * waits for the kernel before it.  The CTAs of a sequence exchange their sums; should these not
+ * arrive within a device wait's limit (2 s), twice, accepted[b] and all of tokens[b] are -1.
+ * Errors: MLA_ERR_ARG, MLA_ERR_CUDA.
  */
 MLA_API int mla_verify_draft(const void *target_probs, const int64_t target_strides[2], const void *draft_probs,
                              const int64_t draft_strides[2], int dtype, const int32_t *draft_tokens,
                              const float *uniform, const float *uniform_new, const int32_t *num_drafts, int batch,
                              int drafts, int vocab, int32_t *accepted, int32_t *tokens, mla_stream_t stream);
+
+/*
+ * mla_verify_draft_selftest -- mla_verify_draft with `timeout_ns` as the limit of its device
+ * waits.  With `missing` not 0 each exchange expects one sum more than is sent, so both waits
+ * give up and every sequence gets -1; with 0 a limit of 0 makes waits give up that would have
+ * succeeded a little later, and the results are those of mla_verify_draft.  Lets a test check the
+ * time-out path without hanging a GPU.  Errors: MLA_ERR_ARG (timeout_ns above 10 s), and as above.
+ */
+MLA_API int mla_verify_draft_selftest(const void *target_probs, const int64_t target_strides[2],
+                                      const void *draft_probs, const int64_t draft_strides[2], int dtype,
+                                      const int32_t *draft_tokens, const float *uniform, const float *uniform_new,
+                                      const int32_t *num_drafts, int batch, int drafts, int vocab, int32_t *accepted,
+                                      int32_t *tokens, uint64_t timeout_ns, int missing, mla_stream_t stream);
 
 /*
  * mla_query_status -- synchronise `stream`, read and clear the workspace status block.

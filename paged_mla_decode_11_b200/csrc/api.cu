@@ -362,6 +362,49 @@ int decode_fp8(const void *q, const int64_t *q_strides, int batch, int s_q, int 
   return MLA_OK;
 }
 
+// missing: sums that the exchange expects beyond those that are sent.
+int verify_draft(const void *target_probs, const int64_t *target_strides, const void *draft_probs,
+                 const int64_t *draft_strides, int dtype, const int32_t *draft_tokens, const float *uniform,
+                 const float *uniform_new, const int32_t *num_drafts, int batch, int drafts, int vocab,
+                 int32_t *accepted, int32_t *tokens, unsigned long long wait_ns, int missing, mla_stream_t stream) {
+  if (!target_probs || !target_strides || (draft_probs && !draft_strides) || !draft_tokens || !uniform ||
+      !uniform_new || !accepted || !tokens)
+    return fail(MLA_ERR_ARG, "null pointer argument");
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  if (batch < 1 || batch > (1 << 24) || drafts < 1 || drafts > (1 << 20) || vocab < 1 || vocab > (1 << 30))
+    return fail(MLA_ERR_ARG, "batch must be in [1, 2^24], drafts in [1, 2^20] and vocab in [1, 2^30]");
+  for (int i = 0; i < 2; ++i)
+    if (target_strides[i] < 0 || (draft_probs && draft_strides[i] < 0))
+      return fail(MLA_ERR_ARG, "strides must be non-negative");
+  const size_t size = dtype == MLA_DTYPE_F32 ? 4 : 2;
+  if (!aligned(target_probs, size) || !aligned(draft_probs, size) || !aligned(draft_tokens, 4) ||
+      !aligned(uniform, 4) || !aligned(uniform_new, 4) || !aligned(num_drafts, 4) || !aligned(accepted, 4) ||
+      !aligned(tokens, 4))
+    return fail(MLA_ERR_ARG, "every tensor must be aligned to its element size");
+  VerifyParams p;
+  p.target = target_probs;
+  p.draft = draft_probs;
+  p.t_b = target_strides[0];
+  p.t_s = target_strides[1];
+  p.d_b = draft_probs ? draft_strides[0] : 0;
+  p.d_s = draft_probs ? draft_strides[1] : 0;
+  p.batch = batch;
+  p.drafts = drafts;
+  p.vocab = vocab;
+  p.tokens = draft_tokens;
+  p.uniform = uniform;
+  p.uniform_new = uniform_new;
+  p.num_drafts = num_drafts;
+  p.accepted = accepted;
+  p.out = tokens;
+  p.wait_ns = wait_ns;
+  p.missing = missing;
+  cudaError_t e = launch_verify(p, dtype, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "draft verification launch");
+  return MLA_OK;
+}
+
 }  // namespace
 
 namespace pagedmla {
@@ -854,40 +897,18 @@ int mla_verify_draft(const void *target_probs, const int64_t target_strides[2], 
                      const int64_t draft_strides[2], int dtype, const int32_t *draft_tokens, const float *uniform,
                      const float *uniform_new, const int32_t *num_drafts, int batch, int drafts, int vocab,
                      int32_t *accepted, int32_t *tokens, mla_stream_t stream) {
-  if (!target_probs || !target_strides || (draft_probs && !draft_strides) || !draft_tokens || !uniform ||
-      !uniform_new || !accepted || !tokens)
-    return fail(MLA_ERR_ARG, "null pointer argument");
-  int rc = check_dtype(dtype);
-  if (rc) return rc;
-  if (batch < 1 || batch > (1 << 24) || drafts < 1 || drafts > (1 << 20) || vocab < 1 || vocab > (1 << 30))
-    return fail(MLA_ERR_ARG, "batch must be in [1, 2^24], drafts in [1, 2^20] and vocab in [1, 2^30]");
-  for (int i = 0; i < 2; ++i)
-    if (target_strides[i] < 0 || (draft_probs && draft_strides[i] < 0))
-      return fail(MLA_ERR_ARG, "strides must be non-negative");
-  const size_t size = dtype == MLA_DTYPE_F32 ? 4 : 2;
-  if (!aligned(target_probs, size) || !aligned(draft_probs, size) || !aligned(draft_tokens, 4) ||
-      !aligned(uniform, 4) || !aligned(uniform_new, 4) || !aligned(num_drafts, 4) || !aligned(accepted, 4) ||
-      !aligned(tokens, 4))
-    return fail(MLA_ERR_ARG, "every tensor must be aligned to its element size");
-  VerifyParams p;
-  p.target = target_probs;
-  p.draft = draft_probs;
-  p.t_b = target_strides[0];
-  p.t_s = target_strides[1];
-  p.d_b = draft_probs ? draft_strides[0] : 0;
-  p.d_s = draft_probs ? draft_strides[1] : 0;
-  p.batch = batch;
-  p.drafts = drafts;
-  p.vocab = vocab;
-  p.tokens = draft_tokens;
-  p.uniform = uniform;
-  p.uniform_new = uniform_new;
-  p.num_drafts = num_drafts;
-  p.accepted = accepted;
-  p.out = tokens;
-  cudaError_t e = launch_verify(p, dtype, reinterpret_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "draft verification launch");
-  return MLA_OK;
+  return verify_draft(target_probs, target_strides, draft_probs, draft_strides, dtype, draft_tokens, uniform, uniform_new,
+                      num_drafts, batch, drafts, vocab, accepted, tokens, kWatchdogNs, 0, stream);
+}
+
+int mla_verify_draft_selftest(const void *target_probs, const int64_t target_strides[2], const void *draft_probs,
+                              const int64_t draft_strides[2], int dtype, const int32_t *draft_tokens,
+                              const float *uniform, const float *uniform_new, const int32_t *num_drafts, int batch,
+                              int drafts, int vocab, int32_t *accepted, int32_t *tokens, uint64_t timeout_ns,
+                              int missing, mla_stream_t stream) {
+  if (timeout_ns > 10ull * 1000000000ull) return fail(MLA_ERR_ARG, "timeout_ns must be at most 10 s");
+  return verify_draft(target_probs, target_strides, draft_probs, draft_strides, dtype, draft_tokens, uniform, uniform_new,
+                      num_drafts, batch, drafts, vocab, accepted, tokens, timeout_ns, missing != 0, stream);
 }
 
 int mla_query_status(void *workspace, mla_stream_t stream) {

@@ -113,6 +113,8 @@ struct VerifyParams {
   const float *uniform, *uniform_new;
   const int32_t *num_drafts;   // nullptr: all of them
   int32_t *accepted, *out;
+  unsigned long long wait_ns;  // limit of a device-side wait
+  int missing;                 // sums expected beyond those that are sent (the self-test: 1)
 };
 cudaError_t launch_verify(const VerifyParams &p, int dtype, cudaStream_t stream);
 

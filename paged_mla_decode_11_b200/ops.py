@@ -47,7 +47,7 @@ EXPORTED = (
     "mla_last_error_string", "mla_decode_paged_static", "mla_query_status_static", "mla_decode_paged_fp8",
     "mla_merge_partials", "mla_absorb_query", "mla_absorb_output", "mla_get_metadata_csr", "mla_decode_sparse",
     "mla_rope", "mla_cache_slots", "mla_cache_write", "mla_cache_write_fp8", "mla_cache_read", "mla_cache_read_fp8",
-    "mla_verify_draft", "mla_decode_paged_fp8_rows",
+    "mla_verify_draft", "mla_verify_draft_selftest", "mla_decode_paged_fp8_rows",
 )
 
 
@@ -107,6 +107,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "mla_cache_read": [P, I64, I, I, P, I64, P, P, P],
             "mla_cache_read_fp8": [P, P, I64, I, I, P, I64, P, P, P],
             "mla_verify_draft": [P, P, P, P, I, P, P, P, P, I, I, I, P, P, P],
+            "mla_verify_draft_selftest": [P, P, P, P, I, P, P, P, P, I, I, I, P, P, U64, I, P],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -703,7 +704,8 @@ def mla_verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uni
     contiguous), draft_tokens int32 [b, s], uniform fp32 [b, s] and uniform_new fp32 [b] in
     [0, 1), draft_probs [b, s, V] of the target's type (None: drafts chosen with certainty),
     num_drafts int32 [b] (None: s everywhere).  Returns (accepted int32 [b], tokens int32
-    [b, s + 1]: the accepted drafts, the next token, then -1)."""
+    [b, s + 1]: the accepted drafts, the next token, then -1).  A sequence whose device-side wait
+    gave up has -1 everywhere."""
     return (_binding or load_binding()).verify_draft(target_probs, draft_tokens, uniform, uniform_new, draft_probs, num_drafts)
 
 

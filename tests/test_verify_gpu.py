@@ -1,6 +1,8 @@
 """Verification of drafted tokens (mla_verify_draft) against the rule written out in fp64, one
 sequence after another.  Results are whole numbers and must be equal."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -165,3 +167,44 @@ def test_streams_graphs_and_repeats():
         counts, made = expected(*new)
         np.testing.assert_array_equal(held[0].cpu().numpy(), counts)
         np.testing.assert_array_equal(held[1].cpu().numpy(), made)
+
+
+def limited(args, timeout_ns, missing):
+    """mla_verify_draft_selftest on the arguments of mla_verify_draft (with draft rows)."""
+    target, tokens, u, u_new, draft = args
+    b, s1, V = target.shape
+    accepted = torch.full((b,), 7, dtype=torch.int32, device="cuda")
+    made = torch.full((b, s1), 7, dtype=torch.int32, device="cuda")
+    strides = [(ctypes.c_int64 * 2)(t.stride(0), t.stride(1)) for t in (target, draft)]
+    kind = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}[target.dtype]
+    rc = ops.load_library().mla_verify_draft_selftest(
+        target.data_ptr(), strides[0], draft.data_ptr(), strides[1], kind, tokens.data_ptr(), u.data_ptr(),
+        u_new.data_ptr(), None, b, s1 - 1, V, accepted.data_ptr(), made.data_ptr(), timeout_ns, missing,
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == ops.MLA_OK
+    torch.cuda.synchronize()
+    return accepted, made
+
+
+@pytest.mark.parametrize("b,s,V", [(1, 1, 32003), (5, 3, 131072), (64, 3, 4096), (300, 1, 129)])
+def test_sums_that_do_not_arrive_leave_no_result(b, s, V):
+    # 2 ms of waiting for one sum that nobody sends: no token is made up, and the next call is as ever
+    args = draw(b, s, V, torch.float32, seed=b)
+    accepted, made = limited(args, 2_000_000, 1)
+    assert (accepted == -1).all() and (made == -1).all()
+    target, tokens, u, u_new, draft = args
+    check(target, tokens, u, u_new, draft)
+
+
+@pytest.mark.parametrize("b,s,V", [(1, 1, 32003), (5, 3, 131072), (64, 3, 4096), (300, 1, 129), (100, 2, 50000)])
+def test_waits_that_give_up_early_change_nothing(b, s, V):
+    # a limit of zero: waits give up while other CTAs still sum, meet them, and find the sums
+    args = draw(b, s, V, torch.float32, seed=b + 1)
+    target, tokens, u, u_new, draft = args
+    target[0, 0] = draft[0, 0] * 0.5                 # nothing left after a rejection: a second exchange
+    u[0, 0] = 0.9
+    counts, made = expected(*args)
+    for _ in range(20):
+        got = limited(args, 0, 0)
+        np.testing.assert_array_equal(got[0].cpu().numpy(), counts)
+        np.testing.assert_array_equal(got[1].cpu().numpy(), made)
