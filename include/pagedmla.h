@@ -231,9 +231,9 @@ MLA_API int mla_decode_paged_fp8(const void *q, const int64_t q_strides[3], int 
  * (s_q * h_q / h_kv up to 2^20): up to 16 it is that call, above 16 a CTA-pair tcgen05 kernel whose
  * products run on the codes themselves.  There the query (per row) and the probabilities times
  * the key scales are each carried as a sum of two 8-bit terms.  The query's sum is exact for
- * values down to 2^-10 of the row's largest and within 2^-18 of the largest below; the
- * probabilities' is within 2^-8 of the value (as a bf16 rounding) or 2^-20 of the row's largest
- * product of a probability and its key's scale.
+ * values down to 2^-9 of the row's largest and within 2^-17 of the largest below; the
+ * probabilities' is within 2^-8 + 2^-11 of the value (a bf16 rounding is within 2^-8) or 2^-20 of
+ * the row's largest product of a probability and its key's scale.
  * k_scale must be finite for every key (a block-table entry outside the pool reads some page of
  * it); a query row that holds an infinity or NaN gives NaN in
  * its own rows only.  Scales below 2^-100 lose precision.  All arguments, layouts, results and

@@ -6,13 +6,15 @@
 // operand into two 8-bit terms whose sum keeps it:
 //   q = 2^-a (q_hi + q_lo)    a the row's own power of two (largest |q| in [128, 256)), q_hi the
 //                             nearest E4M3 value and q_lo, E4M3, the rest.  A bf16 value has 8
-//                             significant bits and E4M3 4: the sum is exact for every |q| above
-//                             2^-10 of the row's largest, below it is off by at most 2^-18 of that
+//                             significant bits and E4M3 4, in steps of 2^-9 at least: the sum is exact
+//                             from 2^-2 on, for every |q| of 2^-9 of the row's largest, and below off by
+//                             at most 2^-10, 2^-17 of the largest
 //   P s = 2^u (v_hi + v_lo)  s the key's scale, u the row's own: its largest P s so far is in [2^6, 2^8]
 //                             units.  v_hi is the nearest E4M3 value, v_lo the rest in E5M2.  For v in
 //                             [2^k, 2^(k+1)) the rest is at most 2^(k-4) and E5M2's half step below that
 //                             2^(k-8): within 2^-8 of the value, as a bf16 rounding of P is, while
-//                             v >= 2^-6; below, within 2^-14, that is 2^-20 of the row's largest.  (A
+//                             v >= 2^-6 (and 2^-11, as both start from v in f16); below, within 2^-14,
+//                             that is 2^-20 of the row's largest.  (A
 //                             unit of the largest scale alone would let a key of no weight in the row,
 //                             such as a row of zeros, which the writer stores with scale 1, push all
 //                             others below 2^-14)

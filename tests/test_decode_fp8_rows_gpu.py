@@ -373,3 +373,26 @@ def test_scales_against_probabilities(h_q, s_q, num_parts, span):
     code = (24 * 2.0 ** (1 - span) * score / torch.exp2(e)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
     x["k8"][:, :, 0, 512] = code
     own_parity(x, num_parts)
+
+
+def test_small_query_elements():
+    """One key of ones, so the LSE is the score, sum(q) / 24, beside one query element of 1.0 that meets a
+    zero.  1.0 becomes 128: an element of 2^-9 or more is 2^-2 or more there and exact; 2^-10 (1 + 2^-7) is
+    2^-3 + 2^-10, half a step of 2^-9 off, 2^-17 of the largest, and the next even code is 2^-3.
+    The score's 36 accumulations round by 2^-23 of it each; 2e-6 for the LSE's log2, sum and product."""
+    x = W.make_inputs_fp8(W.custom(1, 1, 128, 1, [1], causal=False), seed=1)
+    x["k8"].fill_(0x38)
+    x["k8"][..., 0] = 0
+    x["k_scale"].fill_(1.0)
+    x["softmax_scale"] = 1 / 24
+    g = torch.Generator().manual_seed(2)
+    x["q"][0, 0, :64] = 2.0 ** -9 * (1 + torch.randint(0, 128, (64, 576), generator=g) / 128)
+    x["q"][0, 0, 64:] = 2.0 ** -10 * (1 + 2.0 ** -7)
+    x["q"][..., 0] = 1.0
+    want = x["q"][0, 0, :, 1:].double().sum(-1).cuda() / 24
+    _, lse, _ = run(x)
+    off = (lse[0, :, 0].double() - want).abs()
+    slack = 36 * 2.0 ** -23 * want + 2e-6
+    assert (off[:64] <= slack[:64]).all()
+    assert (off[64:] <= 2.0 ** -17 * 575 / 24 + slack[64:]).all()
+    assert (off[64:] > 2.0 ** -18 * 575 / 24 + slack[64:]).all()         # not within half of that
