@@ -62,10 +62,15 @@ def _compile(src: str, verbose: bool, extra: list[str]) -> str:
 
 
 def _build_binding(verbose: bool) -> None:
-    src = os.path.join(CSRC, "binding.cpp")
-    if not _stale(BINDING, [src, os.path.join(INCLUDE, "pagedmla.h")]):
-        return
     import torch
+    src = os.path.join(CSRC, "binding.cpp")
+    # built against one torch and one interpreter: another of either needs another module
+    built_for = f"torch {torch.__version__} cxx11_abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} python {sys.version}"
+    stamp = os.path.join(BUILD, "binding.txt")
+    if not _stale(BINDING, [src, os.path.join(INCLUDE, "pagedmla.h")]) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == built_for:
+                return
     from torch.utils import cpp_extension
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     tmp = BINDING + f".tmp{os.getpid()}"
@@ -82,6 +87,8 @@ def _build_binding(verbose: bool) -> None:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(built_for)
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:

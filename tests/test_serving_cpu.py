@@ -327,3 +327,22 @@ def test_rope_refuses_what_it_cannot_differentiate():
             ops.mla_rope(**rope_args(x=dual, out=z(5, 4, 64)))
         with pytest.raises(ValueError, match="CUDA tensor"):
             ops.mla_rope(**rope_args(x=dual))
+
+
+def test_marshalling_module_is_rebuilt_for_another_torch(monkeypatch, tmp_path):
+    made = []
+
+    def compile_it(cmd, *a, **kw):
+        made.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(B, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(B, "BUILD", str(tmp_path))
+    monkeypatch.setattr(B.subprocess, "check_call", compile_it)
+    B._build_binding(False)
+    B._build_binding(False)
+    assert len(made) == 1
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    B._build_binding(False)
+    B._build_binding(False)
+    assert len(made) == 2
