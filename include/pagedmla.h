@@ -390,7 +390,8 @@ MLA_API int mla_rope(const void *x, const int64_t x_strides[2], int dtype, int64
  * Rows of a prefix to read back are listed by the same call (all L_b tokens as "new").
  *   row_ptr       device int32 [batch + 1], non-decreasing
  *   block_table   device int32 [batch][table_width] with row stride block_table_stride
- *   slots         device int64 [tokens], written; positions device int32 [tokens], written
+ *   slots         device int64 [tokens], written; positions device int32 [tokens], written;
+ *                 apart from each other and from the other arguments
  * tokens = 0 enqueues nothing.  Errors: MLA_ERR_ARG, MLA_ERR_CUDA.
  */
 MLA_API int mla_cache_slots(const int32_t *row_ptr, const int32_t *cache_seqlens, int batch,

@@ -254,7 +254,11 @@ PyObject *cache_slots(PyObject *const *a, Py_ssize_t n) {
       out[i] = &tensor(a[5 + i], names[i]);
       need_type(*out[i], names[i], types[i]);
       need_vector(*out[i], names[i], "tokens", tokens);
+      // one thread's results may be another's arguments
+      if (overlap(*out[i], table) || overlap(*out[i], lens) || overlap(*out[i], ptr))
+        refuse_value(std::string(names[i]) + " must not overlap the arguments");
     }
+  if (given(a[5]) && given(a[6]) && overlap(*out[0], *out[1])) refuse_value("slots and positions must not overlap");
   const Place place(table, "block_table");
   place.same(lens, "cache_seqlens");
   place.same(ptr, "row_ptr");

@@ -658,7 +658,7 @@ def mla_cache_slots(block_table: torch.Tensor, cache_seqlens: torch.Tensor, row_
     """Slots (int64 [tokens]) and positions (int32 [tokens]) of a step's new tokens, numbered
     sequence after sequence by ``row_ptr`` (int32 [b + 1]); those of sequence b are the last of its
     cache_seqlens[b] entries.  Tokens past row_ptr[-1], and any without a page in [0, num_pages),
-    get slot -1.  Buffers may be passed for reuse."""
+    get slot -1.  Buffers may be passed for reuse, apart from each other and from the arguments."""
     return (_binding or load_binding()).cache_slots(block_table, cache_seqlens, row_ptr, num_pages, tokens, slots, positions)
 
 

@@ -346,3 +346,17 @@ def test_marshalling_module_is_rebuilt_for_another_torch(monkeypatch, tmp_path):
     B._build_binding(False)
     B._build_binding(False)
     assert len(made) == 2
+
+
+def test_slots_refuses_outputs_among_its_arguments():
+    words = z(64, dtype=i32)
+    a = dict(block_table=words[:12].view(3, 4), cache_seqlens=words[12:15], row_ptr=words[15:19], num_pages=12, tokens=3)
+    for name, at in (("positions", 14), ("positions", 9), ("positions", 17)):
+        with pytest.raises(ValueError, match="positions must not overlap the arguments"):
+            ops.mla_cache_slots(**a, **{name: words[at:at + 3]})
+    with pytest.raises(ValueError, match="slots must not overlap the arguments"):
+        ops.mla_cache_slots(**a, slots=words[18:24].view(i64))
+    with pytest.raises(ValueError, match="slots and positions"):
+        ops.mla_cache_slots(**a, slots=words[24:30].view(i64), positions=words[29:32])
+    with pytest.raises(ValueError, match="CUDA tensor"):               # beside them is in order
+        ops.mla_cache_slots(**a, slots=words[20:26].view(i64), positions=words[26:29])
