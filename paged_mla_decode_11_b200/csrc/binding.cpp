@@ -494,6 +494,12 @@ PyObject *decode_fp8_rows(PyObject *const *a, Py_ssize_t n) {
       refuse_value("lse must be a contiguous fp32 [b, h_q, s_q] tensor");
     need_writable(*lse, "lse");
   }
+  // a sequence's results are written while others still read
+  for (const auto &[t, name] : {std::pair<const at::Tensor &, const char *>{*out, "out"}, {*lse, "lse"}})
+    if (t.defined() && (overlap(t, q) || overlap(t, k8) || overlap(t, scale) || overlap(t, table) || overlap(t, lens) ||
+                        overlap(t, tile) || overlap(t, splits)))
+      refuse_value(std::string(name) + " must not overlap the arguments");
+  if (out->defined() && lse->defined() && overlap(*out, *lse)) refuse_value("out and lse must not overlap");
   const Place place(q, "q");
   place.same(k8, "k8");
   place.same(scale, "k_scale");

@@ -404,7 +404,8 @@ def mla_decode_paged_fp8_rows(q: torch.Tensor, k8: torch.Tensor, k_scale: torch.
                               skip_combine: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
     """mla_decode_paged_fp8 for any number of query rows per latent head (above 16 a CTA-pair
     tensor-core kernel on the codes themselves).  Without ``workspace`` the (device, stream)'s
-    scratch buffer is used, under CUDA-graph capture one that belongs to the graph."""
+    scratch buffer is used, under CUDA-graph capture one that belongs to the graph.  ``out`` and
+    ``lse`` must lie apart from the arguments and each other."""
     if workspace is None and q.dim() == 4 and k8.dim() == 4 and tile_metadata.dim() == 2 and q.is_cuda:
         b, s_q, h_q, _ = q.shape
         nbytes = workspace_size(b, s_q, h_q, k8.shape[2], tile_metadata.shape[0])

@@ -360,3 +360,21 @@ def test_slots_refuses_outputs_among_its_arguments():
         ops.mla_cache_slots(**a, slots=words[24:30].view(i64), positions=words[29:32])
     with pytest.raises(ValueError, match="CUDA tensor"):               # beside them is in order
         ops.mla_cache_slots(**a, slots=words[20:26].view(i64), positions=words[26:29])
+
+
+def test_decode_rows_refuses_outputs_among_its_arguments():
+    q = z(3, 1, 128, 576)
+    a = dict(q=q, k8=z(10, 64, 1, 576, dtype=torch.uint8), k_scale=z(1, 10, 64, dtype=f32),
+             block_table=z(3, 6, dtype=i32), cache_seqlens=z(3, dtype=i32), dv=512, tile_metadata=z(5, 8, dtype=i32),
+             num_splits=z(4, dtype=i32))
+    inside = q.view(-1)[:3 * 128 * 512].view(3, 1, 128, 512)
+    with pytest.raises(ValueError, match="out must not overlap the arguments"):
+        ops.mla_decode_paged_fp8_rows(**a, out=inside)
+    with pytest.raises(ValueError, match="lse must not overlap the arguments"):
+        ops.mla_decode_paged_fp8_rows(**a, lse=a["k_scale"].view(-1)[:384].view(3, 128, 1))
+    both = z(3 * 128 * 512 + 2 * 384)
+    out, lse = both[:3 * 128 * 512].view(3, 1, 128, 512), both[-768:].view(f32).view(3, 128, 1)
+    with pytest.raises(ValueError, match="out and lse"):
+        ops.mla_decode_paged_fp8_rows(**a, out=out, lse=both[:768].view(f32).view(3, 128, 1))
+    with pytest.raises(ValueError, match="CUDA tensor"):               # beside each other is in order
+        ops.mla_decode_paged_fp8_rows(**a, out=out, lse=lse)
