@@ -72,6 +72,9 @@ void need_vector(const at::Tensor &t, const char *name, const char *what, int64_
 // Contiguous last dimension (of any stride where it has one element).
 bool rows_contiguous(const at::Tensor &t) { return t.stride(-1) == 1 || t.size(-1) <= 1; }
 
+// Stride of a dimension; one of a single element is never stepped over, whatever its stride says.
+int64_t step(const at::Tensor &t, int64_t i) { return t.size(i) > 1 ? t.stride(i) : 0; }
+
 // No element of a [T, H, D] tensor with contiguous rows is reached twice.
 void need_rows_apart(const at::Tensor &t, const char *name) {
   int64_t st[2] = {t.stride(0), t.stride(1)}, n[2] = {t.size(0), t.size(1)};
@@ -218,7 +221,7 @@ PyObject *rope(PyObject *const *a, Py_ssize_t n) {
   else
     fresh = place.empty({T, H, D}, x.scalar_type());
   if (out->numel() > 0) {
-    const int64_t xs[2] = {x.stride(0), x.stride(1)}, os[2] = {out->stride(0), out->stride(1)};
+    const int64_t xs[2] = {step(x, 0), step(x, 1)}, os[2] = {step(*out, 0), step(*out, 1)};
     launch(place, [&](mla_stream_t stream) {
       return api.rope(x.const_data_ptr(), xs, type, T, int(H), int(D), int(freq.size(0)), positions.const_data_ptr(),
                       static_cast<const double *>(freq.const_data_ptr()), magnitude, flags, out->data_ptr(), os, stream);
@@ -342,7 +345,7 @@ PyObject *cache_write(PyObject *const *a, Py_ssize_t n) {
     place.same(*freq, "inv_freq");
   }
   if (T == 0) Py_RETURN_NONE;
-  const int64_t ls[2] = {latent.stride(0), latent.stride(1)}, rs[2] = {rp.stride(0), rp.stride(1)};
+  const int64_t ls[2] = {step(latent, 0), step(latent, 1)}, rs[2] = {step(rp, 0), step(rp, 1)};
   const void *w = weight ? weight->const_data_ptr() : nullptr, *pos = freq ? positions->const_data_ptr() : nullptr;
   const double *f = freq ? static_cast<const double *>(freq->const_data_ptr()) : nullptr;
   const int64_t *at = static_cast<const int64_t *>(slots.const_data_ptr());
@@ -386,7 +389,7 @@ PyObject *cache_read(PyObject *const *a, Py_ssize_t n) {
   else
     fresh = place.empty({T, h_kv, kRow}, at::kBFloat16);
   if (out->numel() > 0) {
-    const int64_t os[2] = {out->stride(0), out->stride(1)};
+    const int64_t os[2] = {step(*out, 0), step(*out, 1)};
     const int64_t *at = static_cast<const int64_t *>(slots.const_data_ptr());
     launch(place, [&](mla_stream_t stream) {
       return scale ? api.cache_read_fp8(pool.const_data_ptr(), static_cast<const float *>(scale->const_data_ptr()), pool.size(0),
@@ -439,8 +442,8 @@ PyObject *verify_draft(PyObject *const *a, Py_ssize_t n) {
   if (num) place.same(*num, "num_drafts");
   at::Tensor accepted = place.empty({b}, at::kInt), made = place.empty({b, s + 1}, at::kInt);
   if (b > 0) {
-    const int64_t ts[2] = {target.stride(0), target.stride(1)};
-    const int64_t ds[2] = {draft ? draft->stride(0) : 0, draft ? draft->stride(1) : 0};
+    const int64_t ts[2] = {step(target, 0), step(target, 1)};
+    const int64_t ds[2] = {draft ? step(*draft, 0) : 0, draft ? step(*draft, 1) : 0};
     launch(place, [&](mla_stream_t stream) {
       return api.verify_draft(target.const_data_ptr(), ts, draft ? draft->const_data_ptr() : nullptr, ds, type,
                               static_cast<const int32_t *>(tokens.const_data_ptr()),

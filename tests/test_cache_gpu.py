@@ -252,3 +252,31 @@ def test_written_cache_decodes_like_the_generators():
     assert (a != b).float().mean() <= 1e-4          # quotients next to the middle of two codes
     ref, ref_lse = ops.mla_decode_paged_fp8(q, mine, scale, table, lens, 512, plan, splits, causal=True)
     assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_strides_of_single_elements_do_not_matter(dtype):
+    # one token of one latent head, cut from rows of an odd width: neither stride is ever stepped over
+    both, slots, kw = draw(1, 1, dtype, 3, seed=8)
+    odd = torch.zeros(1, 7, 577, dtype=dtype, device="cuda")
+    odd[:, :1, :576] = both
+    row = odd[:, :1, :576]
+    assert row.stride() == (7 * 577, 577, 1)
+    pools = [torch.zeros(3, 64, 1, 576, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for pool, r in zip(pools, (both, row)):
+        ops.mla_cache_write(r[..., :512], r[..., 512:], slots, pool, **kw)
+    assert torch.equal(*pools) and pools[0].any()
+    caches = [(torch.zeros(3, 64, 1, 576, dtype=torch.uint8, device="cuda"), torch.ones(1, 3, 64, device="cuda")) for _ in range(2)]
+    for (k8, ks), r in zip(caches, (both, row)):
+        ops.mla_cache_write_fp8(r[..., :512], r[..., 512:], slots, k8, ks, **kw)
+    assert torch.equal(caches[0][0], caches[1][0]) and torch.equal(caches[0][1], caches[1][1])
+    out = torch.zeros(1, 7, 577, dtype=torch.bfloat16, device="cuda")
+    ops.mla_cache_read(pools[0], slots, out=out[:, :1, :576])
+    assert torch.equal(out[:, :1, :576], ops.mla_cache_read(pools[0], slots)) and not out[:, 1:].any()
+    x = odd[:, :1, 512:576]
+    assert torch.equal(ops.mla_rope(x, kw["positions"], kw["inv_freq"]),
+                       ops.mla_rope(x.contiguous(), kw["positions"], kw["inv_freq"]))
+    place = odd[:, :1, 512:576]
+    want = ops.mla_rope(place, kw["positions"], kw["inv_freq"])
+    ops.mla_rope(place, kw["positions"], kw["inv_freq"], out=place)
+    assert torch.equal(place, want) and not odd[:, 1:].any() and not odd[..., 576].any()
