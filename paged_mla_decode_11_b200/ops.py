@@ -262,6 +262,14 @@ def _default_workspace(nbytes: int, device: torch.device) -> torch.Tensor:
     return ws
 
 
+def _capturing(device: torch.device) -> bool:
+    """Whether the device's current stream is being captured (torch asks the current device's)."""
+    if device.index == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def mla_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor,
                      cache_seqlens: torch.Tensor, dv: int, tile_metadata: torch.Tensor,
                      num_splits: torch.Tensor, softmax_scale: Optional[float] = None,
@@ -409,7 +417,7 @@ def mla_decode_paged_fp8_rows(q: torch.Tensor, k8: torch.Tensor, k_scale: torch.
     if workspace is None and q.dim() == 4 and k8.dim() == 4 and tile_metadata.dim() == 2 and q.is_cuda:
         b, s_q, h_q, _ = q.shape
         nbytes = workspace_size(b, s_q, h_q, k8.shape[2], tile_metadata.shape[0])
-        if torch.cuda.is_current_stream_capturing():  # a graph's own: graphs may run side by side
+        if _capturing(q.device):  # a graph's own: graphs may run side by side
             workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
             workspace[:256].zero_()
         else:

@@ -378,3 +378,23 @@ def test_decode_rows_refuses_outputs_among_its_arguments():
         ops.mla_decode_paged_fp8_rows(**a, out=out, lse=both[:768].view(f32).view(3, 128, 1))
     with pytest.raises(ValueError, match="CUDA tensor"):               # beside each other is in order
         ops.mla_decode_paged_fp8_rows(**a, out=out, lse=lse)
+
+
+def test_capture_is_looked_for_on_the_tensors_device(monkeypatch):
+    current = [0]
+
+    class on:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", on)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: current[0] == 1)
+    assert ops._capturing(torch.device("cuda", 1)) and current == [0]
+    assert not ops._capturing(torch.device("cuda", 0))
