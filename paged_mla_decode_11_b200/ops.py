@@ -253,21 +253,27 @@ def new_workspace(nbytes: int, device) -> torch.Tensor:
 _ws_cache: dict = {}
 
 
-def _default_workspace(nbytes: int, device: torch.device) -> torch.Tensor:
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = new_workspace(nbytes, device)
-        _ws_cache[key] = ws
-    return ws
-
-
 def _capturing(device: torch.device) -> bool:
     """Whether the device's current stream is being captured (torch asks the current device's)."""
     if device.index == torch.cuda.current_device():
         return torch.cuda.is_current_stream_capturing()
     with torch.cuda.device(device):
         return torch.cuda.is_current_stream_capturing()
+
+
+def _default_workspace(nbytes: int, device: torch.device) -> torch.Tensor:
+    """The (device, stream)'s scratch buffer, grown as needed.  A captured call gets one of its own: it
+    belongs to the graph, so graphs may run side by side, and a larger call made later cannot free it."""
+    if _capturing(device):
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        ws[:256].zero_()
+        return ws
+    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    ws = _ws_cache.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = new_workspace(nbytes, device)
+        _ws_cache[key] = ws
+    return ws
 
 
 def mla_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor,
@@ -280,8 +286,9 @@ def mla_decode_paged(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.
     block_table [b, w] int32, cache_seqlens [b] int32.  Returns (out [b, s_q, h_q, dv]
     bf16, lse [b, h_q, s_q] fp32).  The default softmax_scale is 576 ** -0.5.
 
-    Without ``workspace`` a per-(device, stream) scratch buffer is reused; calls that may
-    run concurrently on one stream's buffer must pass their own.  ``kernel`` is "auto"
+    Without ``workspace`` a per-(device, stream) scratch buffer is reused, under CUDA-graph capture
+    one that belongs to the graph; calls that may run concurrently on one stream's buffer must pass
+    their own.  ``kernel`` is "auto"
     (the library's choice by shape), "warp_mma", "tcgen05" or "one_sm" (the 1-SM 64-row
     tcgen05 kernel where the CTA-pair kernel would apply)."""
     _require_cuda(q, "q", torch.bfloat16)
@@ -416,12 +423,7 @@ def mla_decode_paged_fp8_rows(q: torch.Tensor, k8: torch.Tensor, k_scale: torch.
     ``lse`` must lie apart from the arguments and each other."""
     if workspace is None and q.dim() == 4 and k8.dim() == 4 and tile_metadata.dim() == 2 and q.is_cuda:
         b, s_q, h_q, _ = q.shape
-        nbytes = workspace_size(b, s_q, h_q, k8.shape[2], tile_metadata.shape[0])
-        if _capturing(q.device):  # a graph's own: graphs may run side by side
-            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device)
-            workspace[:256].zero_()
-        else:
-            workspace = _default_workspace(nbytes, q.device)
+        workspace = _default_workspace(workspace_size(b, s_q, h_q, k8.shape[2], tile_metadata.shape[0]), q.device)
     return (_binding or load_binding()).decode_fp8_rows(q, k8, k_scale, block_table, cache_seqlens, dv, tile_metadata,
                                                         num_splits, softmax_scale, causal, workspace, out, lse,
                                                         skip_combine)

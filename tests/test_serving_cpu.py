@@ -398,3 +398,22 @@ def test_capture_is_looked_for_on_the_tensors_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: current[0] == 1)
     assert ops._capturing(torch.device("cuda", 1)) and current == [0]
     assert not ops._capturing(torch.device("cuda", 0))
+
+
+def test_captured_calls_have_scratch_of_their_own(monkeypatch):
+    class Stream:
+        cuda_stream = 7
+
+    capturing = [False]
+    monkeypatch.setattr(ops, "_ws_cache", {})
+    monkeypatch.setattr(ops, "_capturing", lambda device: capturing[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream)
+    cpu = torch.device("cpu")
+    shared = ops._default_workspace(1000, cpu)
+    assert ops._default_workspace(900, cpu) is shared
+    capturing[0] = True
+    first, second = ops._default_workspace(900, cpu), ops._default_workspace(5000, cpu)
+    assert first is not shared and second is not first and first.numel() >= 900 and second.numel() >= 5000
+    assert not first[:256].any() and not second[:256].any()        # the status block
+    capturing[0] = False
+    assert ops._default_workspace(900, cpu) is shared              # neither replaced nor freed
