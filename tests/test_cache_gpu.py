@@ -280,3 +280,29 @@ def test_strides_of_single_elements_do_not_matter(dtype):
     want = ops.mla_rope(place, kw["positions"], kw["inv_freq"])
     ops.mla_rope(place, kw["positions"], kw["inv_freq"], out=place)
     assert torch.equal(place, want) and not odd[:, 1:].any() and not odd[..., 576].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("exponent", [-30, 0, 14])
+def test_rows_as_given_are_correctly_rounded_quotients(dtype, exponent):
+    """Without a norm the codes are exactly those of the IEEE quotient row / scale: the corrected
+    product is the correctly rounded quotient (and below 1e-24 the kernel divides)."""
+    g = torch.Generator(device="cuda").manual_seed(exponent + 40)
+    T = 20000
+    both = torch.randn(T, 1, 576, generator=g, device="cuda")
+    if dtype == torch.float32:
+        both *= torch.exp2(torch.randint(-60, 61, (T, 1, 1), generator=g, device="cuda").float())
+    both = (both * 2.0 ** (exponent / 2 if dtype == torch.float16 else exponent)).to(dtype)
+    slots = torch.randperm(320 * 64, generator=g, device="cuda")[:T]
+    k8 = torch.zeros(320, 64, 1, 576, dtype=torch.uint8, device="cuda")
+    ks = torch.ones(1, 320, 64, device="cuda")
+    ops.mla_cache_write_fp8(both[..., :512], both[..., 512:], slots, k8, ks)
+    rows = both.float()
+    amax = rows.abs().amax(-1)
+    # numpy divides; torch on CUDA multiplies by the rounded 1 / 448 of a Python scalar
+    scale = torch.from_numpy(amax.cpu().numpy() / np.float32(448)).cuda()
+    scale[scale == 0] = 1
+    assert torch.equal(ks.view(1, -1).t()[slots], scale)
+    want = (rows / scale[..., None]).to(torch.float8_e4m3fn).float()
+    # as values: the corrected product of -0 is (-0 - 0) y + -0, a zero of the other sign
+    assert torch.equal(k8.view(-1, 1, 576)[slots].view(torch.float8_e4m3fn).float(), want)
