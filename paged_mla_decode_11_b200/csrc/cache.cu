@@ -12,9 +12,10 @@
 // Both move each byte once, so HBM bounds a long call and the launch a short one.  Rows with a slot
 // outside the pool are skipped by the write and read as zeros.
 //
-// Measured (B200, graphs of back-to-back calls, scattered slots): write of 64 rows 2.0 us (bf16) and 2.3
-// us (FP8); of 65,521 rows into the FP8 cache (114 MB) 24.5 us, 0.71 of the copy rate.  Read of 7,777
-// bf16 rows (18 MB) 3.8 us; of 65,521 FP8 rows (114 MB) 20.1 us, 0.86 of the copy rate.
+// Measured (B200, calls, scattered slots): write of 64 rows 3.6 us (bf16, 1.9 in a graph) and 3.7 us (FP8,
+// 2.1); of 65,521 rows into the FP8 cache (114 MB) 25.7 us, 0.68 of the copy rate, and into the bf16 cache
+// (151 MB) 28.8 us, 0.80.  Read of 7,777 bf16 rows (18 MB) 3.8 us; of 65,521 FP8 rows (114 MB) 20.4 us, 0.85
+// of the copy rate.  Slots of 64 tokens 2.5 us and of 65,521 (1.3 MB) 3.1 us in a graph: launch and round trips.
 #include <cuda_fp8.h>
 
 #include "launch.h"
@@ -65,8 +66,9 @@ cudaError_t launch_cache_slots(const int32_t *row_ptr, const int32_t *seqlens, i
 // ------------------------------------------------------------------------------------
 // Write: one warp per row.  Lane l holds 16 latent columns in 16-byte accesses of neighbouring
 // lanes, and pair l of the rope columns, so the norm, the scale and the rotation need no shared
-// memory: two warp reductions per row.  A long call is bound by the instructions of the row's
-// arithmetic (about 270 a row, issue slots 58% busy), not by its bytes: a warp therefore takes
+// memory: two warp reductions per row.  A long call is bound by the row's arithmetic, a
+// chain of two reductions and the conversions (about 270 instructions a row, issue slots 57% busy, fixed
+// latencies the main stall), not by its bytes: a warp therefore takes
 // several rows, keeps the weight and its pair's frequency in registers while cp.async brings the next
 // rows to shared memory; products run two to an instruction; and a row is divided by its scale with
 // one division (below).  65,521 rows: 43 us with a warp per row and 18 divisions, 34 us with rows in a

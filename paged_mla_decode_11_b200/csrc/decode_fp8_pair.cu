@@ -33,23 +33,24 @@
 // output in tensor memory: the partner's load and the softmax of a group hide behind the next two
 // groups' scores.
 //
-// Measured (B200): 128 sequences x 128 heads x 4,096 tokens 150 us in short runs (970 TFLOP/s of the
-// formula's flops) and 177 us under the sustained power cap (SM clock 1.6 GHz), where the products'
-// energy sets the clock; the bf16 kernel takes 195 to 205 us.  A group takes about 3,700 cycles, of which
-// its products are issued in 2,250 (36 of the score at 37 cycles, 16 of PV at 56) and two gaps of
-// 600 to 700 lie between a group's score and the PV before it; with the pages in L2 a group takes as long.
-// Kept on the way from 284 us with plan and combine: eight
-// softmax warps instead of four, issue warps that run converged so that descriptors stay uniform (an
-// MMA issued from a divergent lane took 100 cycles instead of 45), barriers polled together, six query
-// loaders that split ahead, output rows transposed between lanes before they are stored, the A tile of
-// PV kept in the operand buffer for its second half and the scales in registers (sustained, with the
-// combine, 193.8 to 191.6 to 190.5 us).  Measured slower: register splits for the loaders (setmaxnreg,
+// Measured (B200): 128 sequences x 128 heads x 4,096 tokens 155 us in short runs (941 TFLOP/s of the
+// formula's flops) and 179 us under the sustained power cap (SM clock 1.6 GHz), where the products'
+// energy sets the clock; 198 us with plan and combine; the bf16 kernel takes 195 to 205 us.  A group takes
+// about 3,640 cycles, of which its products are issued in 2,280.  What is waited for is the way round of a
+// ring stage, 10,800 cycles for the three groups in flight: page load 2,500, score 1,820, softmax 2,700 (of
+// which rescaling O takes 770 in two groups of three), the issuing warp's turn 1,320, PV and the producer's
+// turn 2,480.
+// Kept on the way from 284 us with plan and combine: eight softmax warps instead of four, issue warps
+// that run converged so that descriptors stay uniform (an MMA issued from a divergent lane took 100
+// cycles instead of 45), barriers polled together, six query loaders that split ahead, output rows
+// transposed between lanes before they are stored, the A tile of PV kept in the operand buffer for its
+// second half and the scales in registers (sustained, with the combine, 193.8 to 191.6 to 190.5 us).  Measured slower: register splits for the loaders (setmaxnreg,
 // which spilled), all warps loading the first query, one-lane polls, an L2 prefetch, a fixed order of
 // score and PV with blocking waits (206), barriers polled between the MMAs (204), score and PV issued
 // by two warps (198), paired fp32 arithmetic in the softmax (194.5), looped instead of unrolled MMAs (198).
 // The unit of v by row (see above) costs 2.7% against one of the largest scale (with plan and combine, in
-// turn, 170.8 -> 175.4 us; 33 ragged sequences of two tokens 68.0 -> 71.2); rescaling O takes 4% of either.  The
-// score's maxima and the largest P s exchanged one after the other took 180.2, both behind a barrier
+// turn, 170.8 -> 175.4 us; 33 ragged sequences of two tokens 68.0 -> 71.2); rescaling O takes 4% of either.
+// The score's maxima and the largest P s exchanged one after the other took 180.2, both behind a barrier
 // that tells whether any thread needs them 178.8 to 211.
 //
 // Shared memory (per CTA, 8 KB blocks of 64 rows x 128 bytes, 128-byte swizzle):

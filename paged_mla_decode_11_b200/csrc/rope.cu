@@ -12,8 +12,9 @@
 // address is not a multiple of that it moves one pair at a time.  Columns are rotated in fp32
 // and rounded once.
 //
-// Measured (B200, graphs of back-to-back calls): 128 tokens x 128 heads x 64 bf16 columns (4.2 MB)
-// 2.8 us; 4,093 x 128 x 192 (402 MB) 67.7 us, 5.9 TB/s, 0.91 of the copy rate.  That size took 77 us
+// Measured (B200): 128 tokens x 128 heads x 64 bf16 columns (4.2 MB) 2.8 us in a graph, 4.1 as a call;
+// 4,093 x 128 x 192 (402 MB) 67.8 us in a graph, 69.5 as a call, 0.88 of the copy rate; moved one element
+// at a time 257 x 16 x 600 (9.9 MB) 16.9 us.  The large size took 77 us
 // with ordinary stores (results push inputs out of L2), 97 us with blocks of 512 threads and 86 us with
 // two units a thread (64 registers, fewer blocks).
 #include "launch.h"

@@ -18,9 +18,9 @@
 // 10^5 entries are off by a good part of that.  The order of the sums is fixed by the launch
 // shape, without atomics.
 //
-// Measured (B200, graphs of back-to-back calls): 64 sequences x 3 drafts x 131,072 fp32 entries (50 MB)
+// Measured (B200, graphs and calls alike): 64 sequences x 3 drafts x 131,072 fp32 entries (50 MB)
 // 13.6 us, of which the acceptance takes 2.1, the sums 5 to 6, the exchange and search 1.5 and the last
-// scan 2.2 us; one sequence x 32,003 bf16 entries 6.2 us, a chain of four memory round trips.  The first
+// scan 2.2 us; one sequence x 32,003 bf16 entries 6.1 us, a chain of four memory round trips.  The first
 // took 25 us with two conversions to fp64 an entry, loads in registers and cluster barriers.
 #include <cooperative_groups.h>
 
