@@ -236,7 +236,8 @@ MLA_API int mla_decode_paged_fp8(const void *q, const int64_t q_strides[3], int 
  * the row's largest product of a probability and its key's scale.
  * k_scale must be finite for every key (a block-table entry outside the pool reads some page of
  * it); a query row that holds an infinity or NaN gives NaN in
- * its own rows only.  Scales below 2^-100 lose precision.  All arguments, layouts, results and
+ * its own rows only.  A key that holds a NaN code may give NaN in every row of its sequence, also in
+ * rows that the causal rule hides it from (0 * NaN), and in no other sequence.  Scales below 2^-100 lose precision.  All arguments, layouts, results and
  * other errors as in mla_decode_paged_fp8.
  */
 MLA_API int mla_decode_paged_fp8_rows(const void *q, const int64_t q_strides[3], int batch, int s_q, int h_q,
@@ -406,7 +407,7 @@ MLA_API int mla_cache_slots(const int32_t *row_ptr, const int32_t *cache_seqlens
  *   columns 512..575  rope[t][h], or with inv_freq its 32 pairs turned as by mla_rope
  * rounded to bf16 in k_cache, or stored as E4M3 codes and one scale: scale = max|row| / 448 (1
  * for a row of zeros), code = row / scale to nearest.  The row is formed in fp32; an infinity
- * or NaN becomes a NaN code and does not enter the scale.
+ * or NaN becomes a NaN code and does not enter the scale (a decode shows it in the whole sequence).
  *   latent, rope  device, `dtype` (MLA_DTYPE_*), element (t, h, c) at t * strides[0] + h *
  *                 strides[1] + c (for instance the two column ranges of one projection);
  *                 strides non-negative multiples of 8, 16-byte aligned, apart from the cache

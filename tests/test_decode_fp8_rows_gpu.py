@@ -396,3 +396,15 @@ def test_small_query_elements():
     assert (off[:64] <= slack[:64]).all()
     assert (off[64:] <= 2.0 ** -17 * 575 / 24 + slack[64:]).all()
     assert (off[64:] > 2.0 ** -18 * 575 / 24 + slack[64:]).all()         # not within half of that
+
+
+@pytest.mark.parametrize("num_parts", [None, 1, 3])
+def test_a_key_of_nan_stays_in_its_sequence(num_parts):
+    x = W.make_inputs_fp8(W.custom(4, 2, 64, 1, [300, 1000, 70, 129], causal=True), seed=6)
+    out, lse, _ = run(x, num_parts)
+    x["k8"] = x["k8"].clone()
+    x["k8"][key_at(x, 1, 999)] = 0x7f                          # only the last position sees it
+    out2, lse2, _ = run(x, num_parts)
+    keep = [0, 2, 3]
+    assert torch.equal(out2[keep], out[keep]) and torch.equal(lse2[keep], lse[keep])
+    assert torch.isnan(out2[1, 1]).all() and torch.isnan(lse2[1, :, 1]).all()
