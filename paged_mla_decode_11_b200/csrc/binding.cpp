@@ -99,10 +99,16 @@ bool overlap(const at::Tensor &a, const at::Tensor &b) {
   return a0 < end(b) && b0 < end(a);
 }
 
-// A caller's tensor that the call writes: no gradient goes through that write ...
+// Whether a tensor is being differentiated: it needs a gradient or carries a tangent (forward mode).
+bool differentiated(const at::Tensor &t) {
+  return (c10::GradMode::is_enabled() && t.requires_grad()) ||
+         (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined());
+}
+
+// A caller's tensor that the call writes: no derivative goes through that write ...
 void need_writable(const at::Tensor &t, const char *name) {
-  if (c10::GradMode::is_enabled() && t.requires_grad())
-    refuse_value(std::string(name) + " must not require a gradient: the call writes it");
+  if (differentiated(t))
+    refuse_value(std::string(name) + " must not require a gradient or carry a tangent: the call writes it");
 }
 
 // ... and autograd is told of it, so that a backward pass that saved the tensor raises.
@@ -171,18 +177,13 @@ bool truth(PyObject *o) {
   return v != 0;
 }
 
-// rope_recorded(x, inv_freq, out) -> whether autograd is to record the call: a gradient of x is wanted,
-// or x carries a tangent (forward mode).  Derivatives by the frequencies are refused, and an output.
+// rope_recorded(x, inv_freq, out) -> whether autograd is to record the call, as x is differentiated.
+// Derivatives by the frequencies are refused, and an output where the call is recorded.
 PyObject *rope_recorded(PyObject *const *a, Py_ssize_t n) {
   need_arguments(n, 3);
-  const bool forward = c10::AutogradState::get_tls_state().get_fw_grad_mode(), backward = c10::GradMode::is_enabled();
-  auto differentiated = [&](PyObject *o) {
-    if (!THPVariable_Check(o)) return false;
-    const at::Tensor &t = THPVariable_Unpack(o);
-    return (backward && t.requires_grad()) || (forward && t._fw_grad(0).defined());
-  };
-  if (differentiated(a[1])) refuse_value("the derivative by inv_freq is not formed: detach it");
-  if (!differentiated(a[0])) Py_RETURN_FALSE;
+  auto wanted = [](PyObject *o) { return THPVariable_Check(o) && differentiated(THPVariable_Unpack(o)); };
+  if (wanted(a[1])) refuse_value("the derivative by inv_freq is not formed: detach it");
+  if (!wanted(a[0])) Py_RETURN_FALSE;
   if (given(a[2])) refuse_value("out cannot be given for an x that needs a gradient");
   Py_RETURN_TRUE;
 }

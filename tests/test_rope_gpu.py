@@ -312,3 +312,12 @@ def test_tangent_is_carried(interleaved, inverse):
     # differences of the formula: the tangent is that of the 64-bit map at any step
     ref = rotated(t, pos, freq, *how)
     assert ((moved.double() - ref[0]).abs() <= 2.0 ** -24 * ref[0].abs() + 5e-7 * 1.25 * ref[1]).all()
+
+
+def test_function_transforms_are_refused_by_torch():
+    x, pos = draw(5, 4, 64, torch.float32, seed=1)
+    turn = lambda v: ops.mla_rope(v, pos, ops.rope_frequencies(64, device="cuda"))
+    for call in (lambda: torch.func.grad(lambda v: turn(v).sum())(x), lambda: torch.func.jvp(turn, (x,), (x,)),
+                 lambda: torch.func.vmap(turn)(x[None])):
+        with pytest.raises(RuntimeError):
+            call()

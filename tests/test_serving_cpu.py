@@ -417,3 +417,14 @@ def test_captured_calls_have_scratch_of_their_own(monkeypatch):
     assert not first[:256].any() and not second[:256].any()        # the status block
     capturing[0] = False
     assert ops._default_workspace(900, cpu) is shared              # neither replaced nor freed
+
+
+def test_written_tensors_that_carry_a_tangent_are_refused():
+    import torch.autograd.forward_ad as fwd
+    with fwd.dual_level():
+        dual = lambda *shape: fwd.make_dual(z(*shape), z(*shape))
+        for fn, kw in ((ops.mla_rope, rope_args(out=dual(5, 4, 64))),
+                       (ops.mla_cache_write, write_args(k_cache=dual(3, 64, 1, 576))),
+                       (ops.mla_cache_read, dict(k_cache=z(3, 64, 1, 576), slots=z(6, dtype=i64), out=dual(6, 1, 576)))):
+            with pytest.raises(ValueError, match="carry a tangent"):
+                fn(**kw)
